@@ -339,6 +339,48 @@ hs2_status hs2_cp_localize(int32_t batch, const int64_t *global_offset, const in
 hs2_status hs2_kv_bridge(const hs2_kv_view *kv, const void *hidden, int32_t d_model,
                          const void *w_kv, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Operators around the block ------------------------------------------------------------
+ * What a served token passes through in front of the block's projections and behind them. Codes
+ * are OCP e4m3fn; a matrix [rows, cols] held in codes has float32 scales for blocks of 1 x 128 or
+ * 128 x 128 elements: scales[j * scale_ld + i] belongs to columns [128 j, 128 j + 128) and to row
+ * i (1 x 128) or rows [128 i, 128 i + 128) (128 x 128); the last block of columns or rows may be
+ * shorter. value = scale * code, scale = max|x| / 448 over the block in float32 (1 for an all-zero
+ * block), code = round-to-nearest-even e4m3 of the float32 quotient x / scale: the rule of the
+ * e4m3 cache rows. scale_ld is a multiple of 4 and at least the number of rows (of blocks of 128
+ * rows); scales between that number and scale_ld are never written. Strides count elements
+ * between rows. Serving only: there are no backward forms. */
+
+/* Root-mean-square norm with the residual's addition: for every row
+ *   h = x + residual,  residual_out = h rounded to residual_dtype,
+ *   y = h * weight / sqrt(mean(h^2) + eps)
+ * h, the mean and y in float32, y formed from the unrounded h. Outputs: out (y in out_dtype),
+ * codes + scales (y in e4m3, 1 x 128 blocks), or both.
+ * x: device bf16 [rows, d], 16-byte aligned, x_stride >= d a multiple of 8. residual,
+ * residual_out: device [rows, d] of residual_dtype (HS2_OUT_BF16 or HS2_OUT_F32), both or neither
+ * NULL, 16-byte aligned, residual_stride >= d a multiple of 8. weight: device [d] of weight_dtype,
+ * 16-byte aligned. out: device [rows, d] or NULL, out_stride >= d a multiple of 8. codes: device
+ * [rows, d] or NULL, codes_stride >= d a multiple of 16; scales: device [ceil(d / 128), scale_ld],
+ * NULL exactly when codes is. d: a multiple of 8 in [8, 32768], of 16 with codes. eps finite and
+ * >= 0. rows 0: nothing is launched. residual_out may be residual, and residual_out and out may be
+ * x where type and stride agree; other overlaps of outputs are the caller's error. Strides and
+ * types of NULL arrays are ignored. Asynchronous on `stream`; argument errors return before any
+ * launch. */
+hs2_status hs2_rms_norm(int64_t rows, int32_t d, const void *x, int64_t x_stride,
+                        const void *residual, void *residual_out, int32_t residual_dtype,
+                        int64_t residual_stride, const void *weight, int32_t weight_dtype,
+                        float eps, void *out, int32_t out_dtype, int64_t out_stride, void *codes,
+                        int64_t codes_stride, float *scales, int64_t scale_ld, void *stream);
+
+/* Quantises a bf16 matrix to e4m3 codes and scales: block_rows 1 for activations (1 x 128 blocks),
+ * 128 for weights (128 x 128 blocks). x: device bf16 [rows, cols], 16-byte aligned, x_stride >=
+ * cols a multiple of 8; codes: device [rows, cols], 16-byte aligned, codes_stride >= cols a
+ * multiple of 16; scales: device [ceil(cols / 128), scale_ld]. cols: a multiple of 16 in
+ * [16, 65536]. rows 0: nothing is launched. Asynchronous on `stream`; argument errors return
+ * before any launch. */
+hs2_status hs2_fp8_quantize(int64_t rows, int32_t cols, const void *x, int64_t x_stride,
+                            int32_t block_rows, void *codes, int64_t codes_stride, float *scales,
+                            int64_t scale_ld, void *stream);
+
 /* Exercises the bounded waits of the kernels: one thread waits on an mbarrier that nothing
  * arrives at, gives up after limit_us microseconds (1 .. 2e6) and records HS2_ERR_TIMEOUT in the
  * status word at the start of `workspace` (device, 256-byte aligned, >= 256 bytes), which the

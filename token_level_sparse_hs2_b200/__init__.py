@@ -102,6 +102,11 @@ def lib() -> ctypes.CDLL:
         L.hs2_cp_pack_candidates.argtypes = [V, P, P, P, I64, P, I32, P, I32, I32, P, P]
         L.hs2_cp_merge_select.argtypes = [I32, I32, P, P, I32, I32, P, I32, P, P]
         L.hs2_cp_localize.argtypes = [I32, P, P, P, I32, P, P, I32, P, P]
+        L.hs2_rms_norm.argtypes = [I64, I32, P, I64, P, P, I32, I64, P, I32, F, P, I32, I64, P, I64,
+                                   P, I64, P]
+        L.hs2_fp8_quantize.argtypes = [I64, I32, P, I64, I32, P, I64, P, I64, P]
+        for name in ("hs2_rms_norm", "hs2_fp8_quantize"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("hs2_full_attn", "hs2_score_pass", "hs2_sparse_gather_attn_partial",
                      "hs2_lse_merge", "hs2_cp_pack_candidates", "hs2_cp_merge_select",
                      "hs2_cp_localize"):
@@ -345,6 +350,83 @@ def kv_bridge(cache: KvCache, hidden, w_kv, workspace, stream=None):
         raise ValueError("hidden must be [batch, n_q, d_model] and w_kv [256, d_model]")
     _check(lib().hs2_kv_bridge(cache.ref(), _ptr(hidden), d_model, _ptr(w_kv), _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- operators around the block
+
+def _matrix(name: str, t: torch.Tensor, dtypes, shape=None) -> torch.Tensor:
+    """A [rows, cols] tensor with unit column stride and (if given) this shape."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    return t
+
+
+_WIDE = (torch.bfloat16, torch.float32)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows; a single row's stride is its length rounded up to 16."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+
+
+def _scale_ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 4) * 4
+
+
+def fp8_scales(rows: int, cols: int, block_rows: int = 1, device="cuda") -> torch.Tensor:
+    """An uninitialised float32 scale array for a [rows, cols] matrix of e4m3 codes:
+    [ceil(cols / 128), ceil(rows / block_rows)], with the row stride that the library reads."""
+    blocks = -(-rows // block_rows)
+    return torch.empty((-(-cols // 128), -(-max(blocks, 1) // 4) * 4), dtype=torch.float32,
+                       device=device)[:, :blocks]
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out=None, codes=None,
+             scales=None, stream=None):
+    """Root-mean-square norm with the residual's addition (hs2_rms_norm): h = x + residual,
+    residual_out = h, y = h weight / sqrt(mean(h^2) + eps), given as `out` (bf16 or float32)
+    and / or as e4m3 `codes` with `scales` (fp8_scales) for each 128 columns of a row."""
+    rows, d = _matrix("x", x, (torch.bfloat16,)).shape
+    if weight.dtype not in _WIDE or tuple(weight.shape) != (d,) or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous bf16 or float32 [d] tensor")
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out: both or neither")
+    if residual is not None:
+        _matrix("residual", residual, _WIDE, (rows, d))
+        _matrix("residual_out", residual_out, (residual.dtype,), (rows, d))
+        if _row_stride(residual) != _row_stride(residual_out):
+            raise ValueError("residual and residual_out must have one row stride")
+    if out is not None:
+        _matrix("out", out, _WIDE, (rows, d))
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales: both or neither")
+    if codes is not None:
+        _matrix("codes", codes, _CODES, (rows, d))
+        _matrix("scales", scales, (torch.float32,), (-(-d // 128), rows))
+    _check(lib().hs2_rms_norm(
+        rows, d, _ptr(x), _row_stride(x), _ptr(residual), _ptr(residual_out),
+        OUT_BF16 if residual is None else _out_dtype(residual),
+        0 if residual is None else _row_stride(residual), _ptr(weight), _out_dtype(weight), eps,
+        _ptr(out), OUT_BF16 if out is None else _out_dtype(out),
+        0 if out is None else _row_stride(out), _ptr(codes),
+        0 if codes is None else _row_stride(codes), _ptr(scales),
+        0 if scales is None else _scale_ld(scales), _stream(stream)))
+
+
+def fp8_quantize(x, codes, scales, block_rows: int = 1, stream=None):
+    """e4m3 codes and scales of the bf16 matrix x (hs2_fp8_quantize): block_rows 1 gives each row
+    its own scales (activations), 128 one scale for each 128 x 128 block (weights)."""
+    rows, cols = _matrix("x", x, (torch.bfloat16,)).shape
+    _matrix("codes", codes, _CODES, (rows, cols))
+    _matrix("scales", scales, (torch.float32,), (-(-cols // 128), -(-rows // max(block_rows, 1))))
+    _check(lib().hs2_fp8_quantize(rows, cols, _ptr(x), _row_stride(x), block_rows, _ptr(codes),
+                                  _row_stride(codes), _ptr(scales), _scale_ld(scales),
+                                  _stream(stream)))
 
 
 # ---------------------------------------------------------------- context-parallel pieces

@@ -1384,6 +1384,118 @@ hs2_status hs2_kv_bridge(const hs2_kv_view *kv, const void *hidden, int32_t d_mo
   return st == HS2_OK ? ok() : st;
 }
 
+// ------------------------------------------------------------------ operators around the block
+
+namespace {
+bool out_type(int t) { return t == HS2_OUT_BF16 || t == HS2_OUT_F32; }
+
+hs2_status check_codes(int64_t row_blocks, int cols, const void *codes, int64_t stride,
+                       const float *scales, int64_t scale_ld) {
+  if (!codes || !scales) return fail(HS2_ERR_INVALID_ARG, "codes / scales is NULL");
+  if (!aligned16(codes) || !aligned16(scales))
+    return fail(HS2_ERR_INVALID_ARG, "codes / scales must be 16-byte aligned");
+  if (cols % 16) return fail(HS2_ERR_UNSUPPORTED, "%d columns of codes (a multiple of 16)", cols);
+  if (stride < cols || stride % 16)
+    return fail(HS2_ERR_INVALID_ARG, "codes_stride %lld (a multiple of 16, at least %d)",
+                (long long)stride, cols);
+  if (scale_ld < row_blocks || scale_ld % 4)
+    return fail(HS2_ERR_INVALID_ARG, "scale_ld %lld (a multiple of 4, at least %lld)",
+                (long long)scale_ld, (long long)row_blocks);
+  return HS2_OK;
+}
+
+hs2_status check_rows8(const char *what, const void *p, int64_t stride, int cols) {
+  if (!aligned16(p)) return fail(HS2_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+  if (stride < cols || stride % 8)
+    return fail(HS2_ERR_INVALID_ARG, "%s: row stride %lld (a multiple of 8, at least %d)", what,
+                (long long)stride, cols);
+  return HS2_OK;
+}
+}  // namespace
+
+hs2_status hs2_rms_norm(int64_t rows, int32_t d, const void *x, int64_t x_stride,
+                        const void *residual, void *residual_out, int32_t residual_dtype,
+                        int64_t residual_stride, const void *weight, int32_t weight_dtype,
+                        float eps, void *out, int32_t out_dtype, int64_t out_stride, void *codes,
+                        int64_t codes_stride, float *scales, int64_t scale_ld, void *stream) {
+  hs2_status st;
+  if (rows < 0 || rows > INT32_MAX) return fail(HS2_ERR_INVALID_ARG, "rows %lld out of range", (long long)rows);
+  if (d < 8 || d > 32768 || d % 8)
+    return fail(HS2_ERR_UNSUPPORTED, "d %d (a multiple of 8 in [8, 32768])", d);
+  if (rows == 0) return ok();
+  if (!x || !weight) return fail(HS2_ERR_INVALID_ARG, "x / weight is NULL");
+  if ((st = check_rows8("x", x, x_stride, d)) != HS2_OK) return st;
+  if (!aligned16(weight)) return fail(HS2_ERR_INVALID_ARG, "weight must be 16-byte aligned");
+  if (!out_type(weight_dtype)) return fail(HS2_ERR_INVALID_ARG, "weight_dtype %d", weight_dtype);
+  if (!residual != !residual_out)
+    return fail(HS2_ERR_INVALID_ARG, "residual and residual_out: both or neither");
+  if (residual) {
+    if (!out_type(residual_dtype)) return fail(HS2_ERR_INVALID_ARG, "residual_dtype %d", residual_dtype);
+    if ((st = check_rows8("residual", residual, residual_stride, d)) != HS2_OK) return st;
+    if ((st = check_rows8("residual_out", residual_out, residual_stride, d)) != HS2_OK) return st;
+  }
+  if (!(std::isfinite(eps) && eps >= 0.f)) return fail(HS2_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!out && !codes) return fail(HS2_ERR_INVALID_ARG, "out and codes are both NULL");
+  if (out) {
+    if (!out_type(out_dtype)) return fail(HS2_ERR_INVALID_ARG, "out_dtype %d", out_dtype);
+    if ((st = check_rows8("out", out, out_stride, d)) != HS2_OK) return st;
+  }
+  if (codes || scales) {
+    if ((st = check_codes(rows, d, codes, codes_stride, scales, scale_ld)) != HS2_OK) return st;
+  }
+  NormParams np;
+  memset(&np, 0, sizeof np);
+  np.rows = rows;
+  np.d = d;
+  np.x = x;
+  np.x_stride = x_stride;
+  np.res = residual;
+  np.res_out = residual_out;
+  np.res_f32 = residual_dtype == HS2_OUT_F32;
+  np.res_stride = residual_stride;
+  np.w = weight;
+  np.w_f32 = weight_dtype == HS2_OUT_F32;
+  np.eps = eps;
+  np.out = out;
+  np.out_f32 = out_dtype == HS2_OUT_F32;
+  np.out_stride = out_stride;
+  np.codes = static_cast<uint8_t *>(codes);
+  np.codes_stride = codes_stride;
+  np.scales = scales;
+  np.scale_ld = scale_ld;
+  st = cuda_check(launch_rms_norm(np, static_cast<cudaStream_t>(stream)), "rms norm");
+  return st == HS2_OK ? ok() : st;
+}
+
+hs2_status hs2_fp8_quantize(int64_t rows, int32_t cols, const void *x, int64_t x_stride,
+                            int32_t block_rows, void *codes, int64_t codes_stride, float *scales,
+                            int64_t scale_ld, void *stream) {
+  hs2_status st;
+  if (rows < 0 || rows > INT32_MAX) return fail(HS2_ERR_INVALID_ARG, "rows %lld out of range", (long long)rows);
+  if (cols < 16 || cols > 65536 || cols % 16)
+    return fail(HS2_ERR_UNSUPPORTED, "cols %d (a multiple of 16 in [16, 65536])", cols);
+  if (block_rows != 1 && block_rows != 128)
+    return fail(HS2_ERR_UNSUPPORTED, "block_rows %d (1 or 128)", block_rows);
+  if (rows == 0) return ok();
+  if (!x) return fail(HS2_ERR_INVALID_ARG, "x is NULL");
+  if ((st = check_rows8("x", x, x_stride, cols)) != HS2_OK) return st;
+  if ((st = check_codes((rows + block_rows - 1) / block_rows, cols, codes, codes_stride, scales, scale_ld)) != HS2_OK)
+    return st;
+  QuantParams qp;
+  memset(&qp, 0, sizeof qp);
+  qp.rows = rows;
+  qp.cols = cols;
+  qp.block_rows = block_rows;
+  qp.x = x;
+  qp.x_stride = x_stride;
+  qp.codes = static_cast<uint8_t *>(codes);
+  qp.codes_stride = codes_stride;
+  qp.scales = scales;
+  qp.scale_ld = scale_ld;
+  st = cuda_check(launch_fp8_quantize(qp, static_cast<cudaStream_t>(stream)), "fp8 quantise");
+  return st == HS2_OK ? ok() : st;
+}
+
 hs2_status hs2_selftest_wait_timeout(uint32_t limit_us, void *workspace, size_t workspace_bytes,
                                      void *stream) {
   if (limit_us < 1 || limit_us > 2000000) return fail(HS2_ERR_INVALID_ARG, "limit_us %u outside [1, 2e6]", limit_us);

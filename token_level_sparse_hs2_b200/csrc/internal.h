@@ -141,6 +141,42 @@ struct BridgeMaps {
 };
 cudaError_t launch_kv_bridge(const BridgeMaps &tm, const BridgeParams &p, int grid, cudaStream_t s);
 
+// RMS norm with the residual's addition, and the e4m3 quantiser of its output.
+struct NormParams {
+  int64_t rows;
+  int32_t d;
+  const void *x;              // bf16 [rows, d]
+  int64_t x_stride;
+  const void *res;            // [rows, d] bf16 or fp32, or null
+  void *res_out;
+  int32_t res_f32;
+  int64_t res_stride;
+  const void *w;              // [d] bf16 or fp32
+  int32_t w_f32;
+  float eps;
+  void *out;                  // [rows, d] bf16 or fp32, or null
+  int32_t out_f32;
+  int64_t out_stride;
+  uint8_t *codes;             // e4m3 [rows, d], or null
+  int64_t codes_stride;
+  float *scales;              // [ceil(d / 128), scale_ld]
+  int64_t scale_ld;
+};
+cudaError_t launch_rms_norm(const NormParams &p, cudaStream_t s);
+
+// e4m3 codes and scales of a bf16 matrix, 1 x 128 or 128 x 128 blocks.
+struct QuantParams {
+  int64_t rows;
+  int32_t cols, block_rows;
+  const void *x;
+  int64_t x_stride;
+  uint8_t *codes;
+  int64_t codes_stride;
+  float *scales;
+  int64_t scale_ld;
+};
+cudaError_t launch_fp8_quantize(const QuantParams &p, cudaStream_t s);
+
 // Largest thread-block cluster the sparse layer may use for this cache type and head count.
 int sparse_max_cluster(int kv_dtype, int n_heads);
 

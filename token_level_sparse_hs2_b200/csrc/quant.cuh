@@ -41,4 +41,10 @@ __device__ __forceinline__ uint32_t fp8_pair(float a, float b, float sc, float r
                                   __NV_SATFINITE, __NV_E4M3);
 }
 
+// eight codes of a block whose scale is sc (rc = fp8_row_recip(sc))
+__device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float sc, float rc) {
+  return make_uint2((fp8_pair(v[0], v[1], sc, rc) & 0xffffu) | (fp8_pair(v[2], v[3], sc, rc) << 16),
+                    (fp8_pair(v[4], v[5], sc, rc) & 0xffffu) | (fp8_pair(v[6], v[7], sc, rc) << 16));
+}
+
 }  // namespace hs2
