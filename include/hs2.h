@@ -381,6 +381,25 @@ hs2_status hs2_fp8_quantize(int64_t rows, int32_t cols, const void *x, int64_t x
                             int32_t block_rows, void *codes, int64_t codes_stride, float *scales,
                             int64_t scale_ld, void *stream);
 
+/* Product of two e4m3 matrices with block scales: with kb = ceil(k / 128),
+ *   out[i][j] = sum_{b < kb} a_scale[b][i] * w_scale[b][j / 128] * sum_{l in block b} a[i][l] w[j][l]
+ * Both sums in float32: the inner one on the tensor cores, the outer one in block order (split
+ * over up to 8 contiguous ranges of blocks, joined in order, when there are few tiles), so equal
+ * inputs give equal outputs. out is rounded once to out_dtype.
+ * a: device codes [m, k] with 1 x 128 scales (activations: hs2_rms_norm, hs2_fp8_quantize with
+ * block_rows 1), w: device codes [n, k], output feature x input feature, with 128 x 128 scales
+ * (hs2_fp8_quantize with block_rows 128). Codes 16-byte aligned, lda and ldw >= k multiples of 16;
+ * scales [kb, *_scale_ld], 16-byte aligned. k: a multiple of 16 in [16, 65536]; n in [1, 2^24];
+ * m 0: nothing is launched. out: device [m, n] of out_dtype with row stride ldo >= n, aligned to
+ * its element; with ldo * element size a multiple of 16 and out 16-byte aligned it is stored in
+ * wide pieces. Elements between n and ldo and rows from m on are not written. workspace: device,
+ * 256-byte aligned, >= 256 bytes (the status word hs2_read_device_status reads). Asynchronous on
+ * `stream`; argument errors return before any launch. */
+hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t lda,
+                        const float *a_scale, int64_t a_scale_ld, const void *w, int64_t ldw,
+                        const float *w_scale, int64_t w_scale_ld, void *out, int32_t out_dtype,
+                        int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Exercises the bounded waits of the kernels: one thread waits on an mbarrier that nothing
  * arrives at, gives up after limit_us microseconds (1 .. 2e6) and records HS2_ERR_TIMEOUT in the
  * status word at the start of `workspace` (device, 256-byte aligned, >= 256 bytes), which the

@@ -87,3 +87,40 @@ def test_scale_arrays_have_the_layout_the_library_reads():
     for rows, cols, br, want in ((1, 16, 1, (1, 1, 4)), (5, 4096, 1, (32, 5, 8)), (129, 300, 128, (3, 2, 4))):
         s = hs2.fp8_scales(rows, cols, br, device="cpu")
         assert tuple(s.shape) == want[:2] and s.stride(0) == want[2] and s.stride(1) == 1
+
+
+def ws_ptr():
+    buf = torch.zeros(1024, dtype=torch.uint8)
+    return buf, buf.data_ptr() + (-buf.data_ptr()) % 256
+
+
+GEMM = dict(m=4, n=300, k=256, a=A, lda=256, sa=A, sald=4, w=A, ldw=256, sw=A, swld=4, out=A, ot=BF16, ldo=300, ws=A,
+            wsb=256, stream=None)
+
+
+@pytest.mark.parametrize("change,status,word", [
+    (dict(m=-1), 1, b"m"), (dict(m=2 ** 31), 1, b"m"), (dict(n=0), 2, b"n 0"), (dict(n=2 ** 24 + 1), 2, b"n "),
+    (dict(k=0), 2, b"k 0"), (dict(k=264, lda=272, ldw=272), 2, b"k 264"), (dict(k=65552, lda=65552, ldw=65552), 2, b"k"),
+    (dict(a=None), 1, b"codes"), (dict(a=A + 8), 1, b"aligned"), (dict(lda=248), 1, b"codes_stride"),
+    (dict(lda=264), 1, b"codes_stride"), (dict(sa=None), 1, b"scales"), (dict(sald=3), 1, b"scale_ld"), (dict(sald=6), 1, b"scale_ld"),
+    (dict(w=None), 1, b"w"), (dict(w=A + 1), 1, b"aligned"), (dict(ldw=128), 1, b"codes_stride"), (dict(sw=None), 1, b"w_scale"),
+    (dict(swld=2), 1, b"scale_ld"), (dict(out=None), 1, b"out"), (dict(out=A + 1), 1, b"out"), (dict(ot=F32, out=A + 2), 1, b"out"),
+    (dict(ot=2), 1, b"out_dtype"), (dict(ldo=299), 1, b"ldo"), (dict(ws=None), 1, b"workspace"), (dict(ws=A + 64), 1, b"workspace"),
+    (dict(wsb=255), 3, b"workspace"),
+])
+def test_gemm_refusals(L, change, status, word):
+    refused(L, L.hs2_gemm_fp8, list({**GEMM, **change}.values()), status, word)
+
+
+def test_gemm_without_rows_is_no_work(L):
+    assert L.hs2_gemm_fp8(*{**GEMM, "m": 0, "a": None, "sa": None, "out": None, "ws": None, "wsb": 0}.values()) == 0
+
+
+def test_gemm_binding_refuses_wrong_tensors(L):
+    a, w = torch.zeros((4, 256), dtype=torch.uint8), torch.zeros((300, 256), dtype=torch.uint8)
+    good = dict(a=a, a_scale=hs2.fp8_scales(4, 256, device="cpu"), w=w, w_scale=hs2.fp8_scales(300, 256, 128, device="cpu"),
+                out=torch.zeros((4, 300)), workspace=torch.zeros(256, dtype=torch.uint8))
+    for bad in (dict(a=a.float()), dict(a=a[:, :128]), dict(w=w.t()), dict(a_scale=good["w_scale"]), dict(w_scale=good["a_scale"][:1]),
+                dict(out=torch.zeros((4, 299))), dict(out=torch.zeros((4, 300), dtype=torch.float16)), dict(out=torch.zeros((300, 4)).t())):
+        with pytest.raises((TypeError, ValueError)):
+            hs2.gemm_fp8(**{**good, **bad})

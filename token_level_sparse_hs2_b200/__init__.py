@@ -105,7 +105,9 @@ def lib() -> ctypes.CDLL:
         L.hs2_rms_norm.argtypes = [I64, I32, P, I64, P, P, I32, I64, P, I32, F, P, I32, I64, P, I64,
                                    P, I64, P]
         L.hs2_fp8_quantize.argtypes = [I64, I32, P, I64, I32, P, I64, P, I64, P]
-        for name in ("hs2_rms_norm", "hs2_fp8_quantize"):
+        L.hs2_gemm_fp8.argtypes = [I64, I32, I32, P, I64, P, I64, P, I64, P, I64, P, I32, I64, P, SZ,
+                                   P]
+        for name in ("hs2_rms_norm", "hs2_fp8_quantize", "hs2_gemm_fp8"):
             getattr(L, name).restype = ctypes.c_int
         for name in ("hs2_full_attn", "hs2_score_pass", "hs2_sparse_gather_attn_partial",
                      "hs2_lse_merge", "hs2_cp_pack_candidates", "hs2_cp_merge_select",
@@ -427,6 +429,22 @@ def fp8_quantize(x, codes, scales, block_rows: int = 1, stream=None):
     _check(lib().hs2_fp8_quantize(rows, cols, _ptr(x), _row_stride(x), block_rows, _ptr(codes),
                                   _row_stride(codes), _ptr(scales), _scale_ld(scales),
                                   _stream(stream)))
+
+
+def gemm_fp8(a, a_scale, w, w_scale, out, workspace, stream=None):
+    """out = A W^T of e4m3 codes a [m, k] (1 x 128 scales) and w [n, k] (128 x 128 scales), in
+    float32, rounded to out's type (hs2_gemm_fp8). workspace: at least 256 bytes."""
+    m, k = _matrix("a", a, _CODES).shape
+    n = _matrix("w", w, _CODES, (w.shape[0], k)).shape[0]
+    kb = -(-k // 128)
+    _matrix("a_scale", a_scale, (torch.float32,), (kb, m))
+    _matrix("w_scale", w_scale, (torch.float32,), (kb, -(-n // 128)))
+    _matrix("out", out, _WIDE, (m, n))
+    _check(lib().hs2_gemm_fp8(m, n, k, _ptr(a), _row_stride(a), _ptr(a_scale), _scale_ld(a_scale),
+                              _ptr(w), _row_stride(w), _ptr(w_scale), _scale_ld(w_scale),
+                              _ptr(out), _out_dtype(out), out.stride(0) if m > 1 else n,
+                              _ptr(workspace), workspace.numel() * workspace.element_size(),
+                              _stream(stream)))
 
 
 # ---------------------------------------------------------------- context-parallel pieces

@@ -173,19 +173,6 @@ __device__ __forceinline__ bool dt_wait(const DecodeParams &P, volatile int *abo
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
-// kind::f8f6f4 instruction descriptor: fp32 accumulator, e4m3 A and B, both K-major.
-__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int m, int n) {
-  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate));
-}
-
 // The query operand of sequence b in a slot, K-major with the 128-byte swizzle, one lane per
 // head. bf16: two [32][128 B] halves (dims 0..63, 64..127). e4m3: one [2H][128 B] block, hi in
 // row h and lo in row H + h.

@@ -1496,6 +1496,77 @@ hs2_status hs2_fp8_quantize(int64_t rows, int32_t cols, const void *x, int64_t x
   return st == HS2_OK ? ok() : st;
 }
 
+namespace {
+// 2-D tensor map of a row-major matrix: `cols` elements per row, `ld` elements between rows.
+hs2_status encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *p,
+                     int64_t rows, int64_t cols, int64_t ld, int box_rows, int box_cols,
+                     CUtensorMapSwizzle swizzle, const char *what) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * elem)};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, type, 2, const_cast<void *>(p), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(HS2_ERR_CUDA, "cuTensorMapEncodeTiled(%s) = %d", what, (int)r);
+  return HS2_OK;
+}
+}  // namespace
+
+hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t lda,
+                        const float *a_scale, int64_t a_scale_ld, const void *w, int64_t ldw,
+                        const float *w_scale, int64_t w_scale_ld, void *out, int32_t out_dtype,
+                        int64_t ldo, void *workspace, size_t workspace_bytes, void *stream) {
+  hs2_status st;
+  if (m < 0 || m > INT32_MAX - 256) return fail(HS2_ERR_INVALID_ARG, "m %lld out of range", (long long)m);
+  if (n < 1 || n > (1 << 24)) return fail(HS2_ERR_UNSUPPORTED, "n %d outside [1, 2^24]", n);
+  if (k < 16 || k > 65536 || k % 16)
+    return fail(HS2_ERR_UNSUPPORTED, "k %d (a multiple of 16 in [16, 65536])", k);
+  if (!out_type(out_dtype)) return fail(HS2_ERR_INVALID_ARG, "out_dtype %d", out_dtype);
+  if (m == 0) return ok();
+  if (!w || !w_scale || !out) return fail(HS2_ERR_INVALID_ARG, "w / w_scale / out is NULL");
+  if ((st = check_codes(m, k, a, lda, a_scale, a_scale_ld)) != HS2_OK) return st;
+  if ((st = check_codes((n + 127) / 128, k, w, ldw, w_scale, w_scale_ld)) != HS2_OK) return st;
+  if (ldo < n) return fail(HS2_ERR_INVALID_ARG, "ldo %lld < n = %d", (long long)ldo, n);
+  const int oe = out_dtype == HS2_OUT_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(out) % oe) return fail(HS2_ERR_INVALID_ARG, "out is not aligned to its element");
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign)
+    return fail(HS2_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device buffer");
+  if (workspace_bytes < 256)
+    return fail(HS2_ERR_WORKSPACE, "workspace %zu bytes < 256 required", workspace_bytes);
+  int sms = 0;
+  if ((st = sm_count(&sms)) != HS2_OK) return st;
+  if ((st = get_encoder()) != HS2_OK) return st;
+  GemmParams gp;
+  memset(&gp, 0, sizeof gp);
+  gp.m = (int32_t)m;
+  gp.n = n;
+  gp.kb = (k + 127) / 128;
+  gp.a_scale = a_scale;
+  gp.a_scale_ld = a_scale_ld;
+  gp.w_scale = w_scale;
+  gp.w_scale_ld = w_scale_ld;
+  gp.out = out;
+  gp.out_f32 = out_dtype == HS2_OUT_F32;
+  gp.ldo = ldo;
+  gp.status = static_cast<uint32_t *>(workspace);
+  const int tokens = m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  gp.n_tiles = (n + 127) / 128;
+  gp.m_tiles = (int32_t)((m + tokens - 1) / tokens);
+  const int64_t tiles = (int64_t)gp.n_tiles * gp.m_tiles;
+  gp.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, gp.kb, sms / std::max<int64_t>(1, tiles)}));
+  if (tiles * gp.split > INT32_MAX) return fail(HS2_ERR_UNSUPPORTED, "too many output tiles");
+  GemmMaps tm;
+  if ((st = encode_2d(&tm.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, m, k, lda, tokens, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B, "a")) != HS2_OK) return st;
+  if ((st = encode_2d(&tm.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, n, k, ldw, 128, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B, "w")) != HS2_OK) return st;
+  if ((st = encode_2d(&tm.sa, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a_scale, gp.kb, m, a_scale_ld, 1,
+                      tokens, CU_TENSOR_MAP_SWIZZLE_NONE, "a_scale")) != HS2_OK) return st;
+  st = cuda_check(launch_gemm_fp8_tokens(tokens, tm, gp, static_cast<cudaStream_t>(stream)), "fp8 product");
+  return st == HS2_OK ? ok() : st;
+}
+
 hs2_status hs2_selftest_wait_timeout(uint32_t limit_us, void *workspace, size_t workspace_bytes,
                                      void *stream) {
   if (limit_us < 1 || limit_us > 2000000) return fail(HS2_ERR_INVALID_ARG, "limit_us %u outside [1, 2e6]", limit_us);

@@ -177,6 +177,27 @@ struct QuantParams {
 };
 cudaError_t launch_fp8_quantize(const QuantParams &p, cudaStream_t s);
 
+// e4m3 product with block scales: out [m, n] = A [m, k] . W [n, k]^T.
+struct GemmParams {
+  int32_t m, n, kb;           // kb: blocks of 128 along k
+  int32_t n_tiles, m_tiles;   // of the chosen tile
+  int32_t split;              // CTAs (one cluster) along k per tile
+  const float *a_scale;       // [kb, a_scale_ld]
+  int64_t a_scale_ld;
+  const float *w_scale;       // [kb, w_scale_ld]
+  int64_t w_scale_ld;
+  void *out;
+  int32_t out_f32;
+  int64_t ldo;
+  uint32_t *status;           // cleared by the first CTA
+};
+struct GemmMaps {
+  CUtensorMap a, w;           // codes, boxes of 128 bytes x the tile's rows
+  CUtensorMap sa;             // a_scale, boxes of the tile's tokens x 1
+};
+// tokens per tile: 32, 64 or 128; a tile is 128 output features x that many tokens
+cudaError_t launch_gemm_fp8_tokens(int tokens, const GemmMaps &tm, const GemmParams &p, cudaStream_t s);
+
 // Largest thread-block cluster the sparse layer may use for this cache type and head count.
 int sparse_max_cluster(int kv_dtype, int n_heads);
 
