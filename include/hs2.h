@@ -400,6 +400,26 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
                         const float *w_scale, int64_t w_scale_ld, void *out, int32_t out_dtype,
                         int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
 
+/* The full-attention layer (output and log-sum-exp) for a batch whose sequences share one long
+ * prefix: cache rows [prefix_start, prefix_start + prefix_len) precede every sequence's own rows,
+ * which kv_start / kv_len of the view describe as always (kv_len counts a sequence's own rows
+ * only, its n_q queries included). Query i of sequence b attends to the whole prefix and to the
+ * own positions [0, T_b - n_q + i]:
+ *   lse = log( sum_prefix exp(c q.k_t) + sum_own exp(c q.k_t) ),  out = sum exp(c q.k_t - lse) v_t
+ * The prefix's rows are read once for all rows of the batch, not once per sequence. The shared
+ * rows may lie anywhere in the cache; kv_rows bounds them too. prefix_len 0: the own rows alone.
+ * Cache rows outside the prefix and the sequences are not used, whatever they hold. Both parts
+ * are joined from float32. hs2_score_pass takes the lse for the scores of either part (a view of
+ * the own rows, and one whose every sequence is the prefix).
+ * q: device bf16 [B, n_q, H, 128]; out: device [B, n_q, H, 128] of out_dtype; both 16-byte
+ * aligned. lse: device fp32 [B, n_q, H] or NULL. workspace: device, 256-byte aligned, at least
+ * hs2_prefix_attn_workspace_size bytes; its contents on entry do not matter. Asynchronous on
+ * `stream`; argument errors return before any launch. */
+hs2_status hs2_prefix_attn_workspace_size(const hs2_kv_view *kv, int32_t prefix_len, size_t *bytes);
+hs2_status hs2_prefix_attn(const hs2_kv_view *kv, int64_t prefix_start, int32_t prefix_len,
+                           const void *q, float softmax_scale, void *out, int32_t out_dtype,
+                           float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Exercises the bounded waits of the kernels: one thread waits on an mbarrier that nothing
  * arrives at, gives up after limit_us microseconds (1 .. 2e6) and records HS2_ERR_TIMEOUT in the
  * status word at the start of `workspace` (device, 256-byte aligned, >= 256 bytes), which the

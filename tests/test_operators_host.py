@@ -124,3 +124,46 @@ def test_gemm_binding_refuses_wrong_tensors(L):
                 dict(out=torch.zeros((4, 299))), dict(out=torch.zeros((4, 300), dtype=torch.float16)), dict(out=torch.zeros((300, 4)).t())):
         with pytest.raises((TypeError, ValueError)):
             hs2.gemm_fp8(**{**good, **bad})
+
+
+def prefix_call(L, c, start=5, length=100, q=A, scale=0.1, out=A, ot=F32, lse=A, ws=A, wsb=1 << 40):
+    return L.hs2_prefix_attn(c.ref(), start, length, q, ctypes.c_float(scale), out, ot, lse, ws, wsb, None)
+
+
+@pytest.mark.parametrize("change,status,word", [
+    (dict(start=-1), 1, b"prefix rows"), (dict(start=909), 1, b"prefix rows"), (dict(length=-1), 1, b"prefix_len"),
+    (dict(length=1009), 1, b"prefix_len"), (dict(q=None), 1, b"q / out"), (dict(out=None), 1, b"q / out"), (dict(q=A + 8), 1, b"aligned"),
+    (dict(out=A + 4), 1, b"aligned"), (dict(scale=0.0), 1, b"softmax_scale"), (dict(scale=float("inf")), 1, b"softmax_scale"),
+    (dict(ot=7), 1, b"out_dtype"), (dict(ws=None), 1, b"workspace"), (dict(ws=A + 16), 1, b"workspace"), (dict(wsb=4096), 3, b"required"),
+])
+def test_prefix_refusals(L, change, status, word):
+    k = torch.zeros((1008, 128), dtype=torch.bfloat16)
+    c = hs2.KvCache(k, k, [200, 500], [100, 300], 1, 32)
+    got = prefix_call(L, c, **change)
+    assert got == status and word in L.hs2_last_error(), (got, L.hs2_last_error())
+
+
+def test_prefix_workspace_covers_the_plan(L):
+    k = torch.zeros((200000, 128), dtype=torch.bfloat16)
+    sizes = [hs2.prefix_attn_workspace_size(hs2.KvCache(k, k, [150000], [100], 1, 32), p) for p in (0, 1000, 100000)]
+    # the status word; then O and log-sum-exp of 32 rows for each range of at least two
+    assert sizes[0] >= 256 and sizes[1] >= 256 + 2 * 32 * 129 * 4 and sizes[1] < sizes[2]
+    bad = hs2.KvCache(k, k, [150000], [100], 1, 32)
+    bad.view.n_heads = 8
+    with pytest.raises(hs2.HS2Error):
+        hs2.prefix_attn_workspace_size(bad, 10)
+    with pytest.raises(hs2.HS2Error):
+        hs2.prefix_attn_workspace_size(hs2.KvCache(k, k, [150000], [100], 1, 32), 200001)
+
+
+def test_prefix_binding_refuses_wrong_tensors(L):
+    k = torch.zeros((1008, 128), dtype=torch.bfloat16)
+    c = hs2.KvCache(k, k, [200, 500], [100, 300], 1, 32)
+    q, lse = torch.zeros((2, 1, 32, 128), dtype=torch.bfloat16), torch.zeros((2, 1, 32))
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    for bad in (dict(q=q.float()), dict(q=q[:1]), dict(q=q.transpose(0, 1)), dict(out=q[:, :, :16]), dict(out=q.half()),
+                dict(lse=lse.double()), dict(lse=lse[0])):
+        args = dict(q=q, out=q.clone(), lse=lse)
+        args.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            hs2.prefix_attn(c, 5, 100, args["q"], args["out"], args["lse"], ws)

@@ -107,7 +107,10 @@ def lib() -> ctypes.CDLL:
         L.hs2_fp8_quantize.argtypes = [I64, I32, P, I64, I32, P, I64, P, I64, P]
         L.hs2_gemm_fp8.argtypes = [I64, I32, I32, P, I64, P, I64, P, I64, P, I64, P, I32, I64, P, SZ,
                                    P]
-        for name in ("hs2_rms_norm", "hs2_fp8_quantize", "hs2_gemm_fp8"):
+        L.hs2_prefix_attn_workspace_size.argtypes = [V, I32, ctypes.POINTER(SZ)]
+        L.hs2_prefix_attn.argtypes = [V, I64, I32, P, F, P, I32, P, P, SZ, P]
+        for name in ("hs2_rms_norm", "hs2_fp8_quantize", "hs2_gemm_fp8",
+                     "hs2_prefix_attn_workspace_size", "hs2_prefix_attn"):
             getattr(L, name).restype = ctypes.c_int
         for name in ("hs2_full_attn", "hs2_score_pass", "hs2_sparse_gather_attn_partial",
                      "hs2_lse_merge", "hs2_cp_pack_candidates", "hs2_cp_merge_select",
@@ -445,6 +448,29 @@ def gemm_fp8(a, a_scale, w, w_scale, out, workspace, stream=None):
                               _ptr(out), _out_dtype(out), out.stride(0) if m > 1 else n,
                               _ptr(workspace), workspace.numel() * workspace.element_size(),
                               _stream(stream)))
+
+
+def prefix_attn_workspace_size(cache: KvCache, prefix_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().hs2_prefix_attn_workspace_size(cache.ref(), prefix_len, ctypes.byref(n)))
+    return int(n.value)
+
+
+def prefix_attn(cache: KvCache, prefix_start: int, prefix_len: int, q, out, lse, workspace,
+                scale=None, stream=None):
+    """Full-attention output and lse (None: not wanted) of a batch whose sequences share the cache
+    rows [prefix_start, prefix_start + prefix_len), read once for all of them, and go on with
+    their own rows, which `cache` describes (hs2_prefix_attn)."""
+    scale = default_scale() if scale is None else scale
+    shape = (cache.batch, cache.n_q, cache.n_heads)
+    if q.dtype != torch.bfloat16 or (lse is not None and lse.dtype != torch.float32):
+        raise TypeError("q must be bfloat16 and lse float32")
+    for name, t, want in (("q", q, shape + (128,)), ("out", out, shape + (128,)), ("lse", lse, shape)):
+        if t is not None and (tuple(t.shape) != want or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {list(want)}")
+    _check(lib().hs2_prefix_attn(cache.ref(), prefix_start, prefix_len, _ptr(q), scale, _ptr(out),
+                                 _out_dtype(out), _ptr(lse), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 # ---------------------------------------------------------------- context-parallel pieces

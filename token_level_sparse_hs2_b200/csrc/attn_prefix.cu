@@ -1,0 +1,647 @@
+// attn_prefix.cu -- full attention of a batch whose sequences share a prefix.
+//
+// With one K/V head, every (sequence, query token, head) row of the batch meets the same prefix
+// rows, so the batch is one product with R = B n_q H rows and the prefix is read once for all
+// of them. Each CTA takes two blocks of 128 consecutive rows (so that a K/V tile is read from L2
+// once for 256 rows) and a contiguous range of their 128-row K/V tiles: the prefix's, then the
+// own tiles of each sequence that has rows in the pair, up to the last position its rows see. Per
+// tile i and block g:
+//   S_g = Q_g . K_i^T            tcgen05.mma, both operands in shared memory, D in TMEM
+//   P_g = exp2(c log2e S_g - m)  four softmax warps per block, one row per thread: the row's
+//                                running maximum m, the exponentials, the row sum; P is written
+//                                over S as bf16 pairs
+//   O_g += P_g . V_i             tcgen05.mma, A = P (TMEM), B = V tile (MN-major)
+// The blocks alternate on the tensor cores: while block 0's softmax runs, they compute block 1's
+// products. An own tile concerns the lanes of its sequence alone: blocks without such rows skip
+// it, and the product leaves the other lanes of O untouched (its output-lane mask), so a row never
+// meets another sequence's values. The reference maximum only moves when a tile's row maximum
+// exceeds it by more than 8 (P <= 2^8); then the row of O is rescaled in TMEM. P is rounded to
+// bf16 (the tensor cores take no wider operand next to bf16 V; half a step, 2^-8 of each weight,
+// averaged over the keys); m, the sums and O are float32.
+//
+// An e4m3 cache (value = scale[t] code): four more warps widen the code tiles to bf16 (exact);
+// the K scale multiplies S's column, the V scale the weight before its rounding.
+//
+// Rows of a tile behind the prefix's or the sequence's last never count, whatever the cache
+// holds there: their columns are masked, and their V rows are zero (the prefix's tensor maps end at its
+// last row; of an own tile they are cleared in shared memory), so that 0 x NaN does not arise.
+//
+// With more than one range per pair each CTA writes its rows' O and log-sum-exp, which
+// prefix_merge_kernel joins.
+#include "attn_pipeline.cuh"
+#include "internal.h"
+#include "tc05.cuh"
+
+namespace hs2 {
+
+namespace {
+
+constexpr int kPxTile = 128;                       // prefix rows per tile
+constexpr int kPxRows = 128;                       // (query, head) rows per block
+constexpr int kPxTileBytes = kPxTile * 256;        // two [128][128 B] swizzled dim blocks
+constexpr int kPxRawBytes = kPxTile * 128;         // a tile of codes
+constexpr float kPxLazy = 8.f;
+constexpr int kPxWarpMma = 8, kPxWarpTma = 9, kPxWarpWiden = 10;
+constexpr uint32_t kPxCols = 512;                  // S/P at 0 and 128, O at 256 and 384
+
+template <int KV>
+struct PxCfg {
+  static constexpr bool kFp8 = KV == kKvFp8;
+  static constexpr int kThreads = (kFp8 ? 14 : 10) * 32;
+  static constexpr int kSlots = kFp8 ? 4 : 5;      // ring of bf16 tiles: K_0, V_0, K_1, V_1, ...
+  static constexpr int kRaw = kFp8 ? 2 : 0;        // ring of code tiles
+  static constexpr int kScaleSlots = kFp8 ? 3 : 0; // the scales of the tiles in flight
+  static constexpr size_t kBytes = 1024 + 2 * (size_t)kPxRows * 256 + (size_t)kSlots * kPxTileBytes +
+                                   (size_t)kRaw * kPxRawBytes + (size_t)kScaleSlots * kPxTile * 4 +
+                                   (2 * 5 + 2 * 2 + 2 * 3 + 5) * 8 + 16;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+template <int KV>
+struct PxSmem {
+  using C = PxCfg<KV>;
+  uint8_t *q, *ring, *raw;
+  float *scale;
+  uint64_t *full, *empty, *raw_full, *raw_empty, *sc_full, *sc_empty, *s_full, *p_full, *done;
+  uint32_t *tmem_base;
+  volatile int *abort_flag;
+  __device__ explicit PxSmem(uint8_t *p) {
+    q = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+    ring = q + 2 * kPxRows * 256;
+    raw = ring + C::kSlots * kPxTileBytes;
+    scale = reinterpret_cast<float *>(raw + C::kRaw * kPxRawBytes);
+    full = reinterpret_cast<uint64_t *>(scale + C::kScaleSlots * kPxTile);
+    empty = full + 5;
+    raw_full = empty + 5;
+    raw_empty = raw_full + 2;
+    sc_full = raw_empty + 2;
+    sc_empty = sc_full + 3;
+    s_full = sc_empty + 3;
+    p_full = s_full + 2;
+    done = p_full + 2;
+    tmem_base = reinterpret_cast<uint32_t *>(done + 1);
+    abort_flag = reinterpret_cast<volatile int *>(tmem_base + 1);
+  }
+};
+
+// The pair's rows, and a walk over its tiles: the prefix's, then each sequence's own.
+struct PxWalk {
+  int64_t row0;               // first row of the pair
+  int b_last, i_last;         // sequence and query token of its last row
+  int t;                      // tile of the list
+  int b, j, count;            // own tiles: sequence, tile j of its count
+
+  __device__ __forceinline__ int own_tiles(const PrefixParams &P, int seq) const {
+    const int i = seq == b_last ? i_last : P.n_q - 1;
+    return (P.seq.len[seq] - P.n_q + i) / kPxTile + 1;
+  }
+  __device__ __forceinline__ PxWalk(const PrefixParams &P, int pair) {
+    row0 = (int64_t)pair * 2 * kPxRows;
+    const int64_t last = min(P.rows, row0 + 2 * kPxRows) - 1;
+    const int q = (int)(last / P.n_heads);
+    b_last = q / P.n_q;
+    i_last = q - b_last * P.n_q;
+    b = (int)(row0 / P.n_heads) / P.n_q;
+    t = j = 0;
+    count = own_tiles(P, b);
+  }
+  __device__ __forceinline__ int total(const PrefixParams &P) const {
+    int n = P.n_tiles;
+    for (int s = b; s <= b_last; ++s) n += own_tiles(P, s);
+    return n;
+  }
+  __device__ __forceinline__ void seek(const PrefixParams &P, int tile) {
+    t = tile;
+    j = tile - P.n_tiles;
+    while (j >= count && b < b_last) {
+      j -= count;
+      count = own_tiles(P, ++b);
+    }
+  }
+  __device__ __forceinline__ void next(const PrefixParams &P) {
+    ++t;
+    if (++j >= count && t > P.n_tiles && b < b_last) {
+      j = 0;
+      count = own_tiles(P, ++b);
+    }
+  }
+  __device__ __forceinline__ bool own(const PrefixParams &P) const { return t >= P.n_tiles; }
+  // rows of the tile that exist for this pair (may exceed the tile)
+  __device__ __forceinline__ int valid(const PrefixParams &P) const {
+    if (!own(P)) return P.prefix_len - t * kPxTile;
+    return P.seq.len[b] - P.n_q + (b == b_last ? i_last : P.n_q - 1) + 1 - j * kPxTile;
+  }
+  // lanes [lo, hi) of block g that see some row of the tile
+  __device__ __forceinline__ void lanes(const PrefixParams &P, int g, int &lo, int &hi) const {
+    const int64_t r0 = row0 + g * kPxRows;
+    hi = (int)min((int64_t)kPxRows, P.rows - r0);
+    lo = 0;
+    if (own(P)) {
+      const int i = max(0, j * kPxTile - (P.seq.len[b] - P.n_q));   // first query token that reaches it
+      lo = (int)max((int64_t)0, ((int64_t)b * P.n_q + i) * P.n_heads - r0);
+      hi = (int)min((int64_t)hi, ((int64_t)b + 1) * P.n_q * P.n_heads - r0);
+    }
+  }
+};
+
+// bounded wait by lane 0, the result broadcast to the warp (records a timeout)
+__device__ __forceinline__ bool px_wait(const PrefixParams &P, volatile int *abort_flag,
+                                        uint64_t *bar, uint32_t parity) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    ok = mbar_wait(smem_u32(bar), parity);
+    if (!ok) {
+      record_status(P.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    if (*abort_flag) ok = false;
+  }
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// 32 scores of this thread's row: columns of S from TMEM, times their K scales (e4m3), -inf from
+// column `valid` on.
+template <bool kFp8>
+__device__ __forceinline__ void px_scores(uint32_t addr, const float *ksc, int valid, float (&x)[32]) {
+  tmem_ld32(addr, x);
+  tmem_wait_ld();
+  if (kFp8) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(ksc + i);
+      const float2 a = fmul2(make_float2(x[i], x[i + 1]), make_float2(f.x, f.y));
+      const float2 b = fmul2(make_float2(x[i + 2], x[i + 3]), make_float2(f.z, f.w));
+      x[i] = a.x;
+      x[i + 1] = a.y;
+      x[i + 2] = b.x;
+      x[i + 3] = b.y;
+    }
+  }
+  if (valid < 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= valid) x[i] = -INFINITY;
+  }
+}
+
+template <int KV>
+__global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ PrefixMaps tm, const __grid_constant__ PrefixParams P) {
+  using C = PxCfg<KV>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  PxSmem<KV> sm(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // neighbouring CTAs take the same tiles for different rows, so that these are read from HBM once
+  const int pair = blockIdx.x % P.n_pairs, split = blockIdx.x / P.n_pairs;
+  PxWalk W(P, pair);
+  const int total = W.total(P);
+  const int tile0 = (int)((int64_t)split * total / P.n_splits);
+  const int n = (int)((int64_t)(split + 1) * total / P.n_splits) - tile0;
+  const int64_t row0 = W.row0;
+  const int nb = P.rows - row0 > kPxRows ? 2 : 1;   // blocks with rows
+  W.seek(P, tile0);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), C::kFp8 ? 4 : 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+    }
+    for (int s = 0; s < C::kRaw; ++s) {
+      mbar_init(smem_u32(&sm.raw_full[s]), 1);
+      mbar_init(smem_u32(&sm.raw_empty[s]), 4);
+    }
+    for (int s = 0; s < C::kScaleSlots; ++s) {
+      mbar_init(smem_u32(&sm.sc_full[s]), 32);
+      mbar_init(smem_u32(&sm.sc_empty[s]), 4 * nb);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(smem_u32(&sm.s_full[g]), 1);
+      mbar_init(smem_u32(&sm.p_full[g]), 4);
+    }
+    mbar_init(smem_u32(&sm.done[0]), 1);
+    *sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kPxWarpTma && lane == 0) {
+    prefetch_tensormap(&tm.pk);
+    prefetch_tensormap(&tm.pv);
+    prefetch_tensormap(&tm.k);
+    prefetch_tensormap(&tm.v);
+  }
+  if (warp == kPxWarpMma) {
+    tmem_alloc(smem_u32(sm.tmem_base), kPxCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem_base;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
+
+  const int g = warp >> 2;                             // softmax warps: the block
+  const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  if (warp < 8) {   // Q blocks -> shared memory (K-major, 128-byte swizzle), zeros behind the last row
+    const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(P.q) + row0 * kHeadDim;
+    const int64_t left = P.rows - row0;
+#pragma unroll 8
+    for (int t = threadIdx.x; t < 2 * kPxRows * 16; t += 256) {
+      const int r = t >> 4, ch = t & 15;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < left) v = *reinterpret_cast<const uint4 *>(qg + (size_t)r * kHeadDim + ch * 8);
+      *reinterpret_cast<uint4 *>(sm.q + (r >> 7) * (kPxRows * 256) + (ch >> 3) * (kPxRows * 128) +
+                                 sw128(r & 127, (ch & 7) * 16)) = v;
+    }
+    fence_proxy_async_smem();
+    if (g < nb) {   // O = 0: every product accumulates, on the lanes that it concerns
+      const uint32_t zero[32] = {};
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) tmem_st32(lane_addr + 256 + g * 128 + c, zero);
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    asm volatile("bar.arrive 1, 288;" ::: "memory");   // the MMA warp waits for these alone
+  }
+
+  float m_run = -INFINITY, l_run = 0.f;
+  if (warp == kPxWarpTma) {
+    // ------------------------------------------------------------ producer
+    int it = 0;
+    for (; it < 2 * n; ++it) {   // K_0, V_0, K_1, V_1, ...
+      const bool own = W.own(P), is_v = it & 1;
+      const CUtensorMap *map = own ? (is_v ? &tm.v : &tm.k) : (is_v ? &tm.pv : &tm.pk);
+      const int y = own ? (int)P.seq.start[W.b] + W.j * kPxTile : W.t * kPxTile;
+      if constexpr (!C::kFp8) {
+        const int s = it % C::kSlots;
+        if (it >= C::kSlots && !px_wait(P, sm.abort_flag, &sm.empty[s], ((it / C::kSlots) & 1) ^ 1)) break;
+        if (lane == 0) {
+          const uint32_t st = smem_u32(sm.ring + s * kPxTileBytes), bar = smem_u32(&sm.full[s]);
+          mbar_arrive_expect_tx(bar, kPxTileBytes);
+          tma_load_2d(st, map, bar, 0, y);
+          tma_load_2d(st + kPxTile * 128, map, bar, 64, y);
+        }
+      } else {
+        const int s = it % C::kRaw, c = it % C::kScaleSlots;
+        if (it >= C::kRaw && !px_wait(P, sm.abort_flag, &sm.raw_empty[s], ((it / C::kRaw) & 1) ^ 1)) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sm.raw_full[s]);
+          mbar_arrive_expect_tx(bar, kPxRawBytes);
+          tma_load_2d(smem_u32(sm.raw + s * kPxRawBytes), map, bar, 0, y);
+        }
+        if (it >= C::kScaleSlots && !px_wait(P, sm.abort_flag, &sm.sc_empty[c], ((it / C::kScaleSlots) & 1) ^ 1)) break;
+        const float *sc = (is_v ? P.v_scale : P.k_scale) + (own ? 0 : P.prefix_start) + y;
+        const int valid = W.valid(P);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 32 + lane;
+          const bool in = r < valid;
+          cp_async_4(smem_u32(sm.scale + c * kPxTile + r), sc + (in ? r : 0), in ? 4u : 0u);
+        }
+        cp_async_mbar_arrive(smem_u32(&sm.sc_full[c]));
+      }
+      if (is_v) W.next(P);
+      __syncwarp();
+    }
+    if (it < 2 * n && lane == 0) {   // gave up: the copies in flight land before the CTA ends
+      constexpr int N = C::kFp8 ? C::kRaw : C::kSlots;
+      for (int j = max(0, it - N); j < it; ++j)
+        mbar_wait(smem_u32(C::kFp8 ? &sm.raw_full[j % N] : &sm.full[j % N]), (j / N) & 1);
+    }
+    if constexpr (C::kFp8) asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  } else if (C::kFp8 && warp >= kPxWarpWiden) {
+    // ------------------------------------------------------------ e4m3 codes -> bf16 tiles
+    // 16 codes per thread and step: eight neighbouring threads take four chunks of two rows, which
+    // the swizzle spreads over all banks
+    const int t = threadIdx.x - kPxWarpWiden * 32;
+    for (int it = 0; it < 2 * n; ++it) {
+      const int r = it % 2, s = it % C::kSlots;
+      if (!px_wait(P, sm.abort_flag, &sm.raw_full[r], (it / 2) & 1)) break;
+      if (it >= C::kSlots && !px_wait(P, sm.abort_flag, &sm.empty[s], ((it / C::kSlots) & 1) ^ 1)) break;
+      const int valid = W.valid(P);
+      const uint8_t *src = sm.raw + r * kPxRawBytes;
+      uint8_t *dst = sm.ring + s * kPxTileBytes;
+#pragma unroll 2
+      for (int u = 0; u < 8; ++u) {
+        const int e = u * 128 + t;                     // (row pair, half, row of the pair, chunk)
+        const int row = (e >> 4) * 2 + ((e >> 2) & 1), ch = ((e >> 3) & 1) * 4 + (e & 3);
+        uint4 c = *reinterpret_cast<const uint4 *>(src + row * 128 + ch * 16);
+        if (row >= valid) c = make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          o[2 * j] = e4m3x2_to_bf16x2((uint16_t)(w[j] & 0xffffu));
+          o[2 * j + 1] = e4m3x2_to_bf16x2((uint16_t)(w[j] >> 16));
+        }
+        uint8_t *box = dst + (ch >> 2) * (kPxTile * 128);
+        *reinterpret_cast<uint4 *>(box + sw128(row, (ch & 3) * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(box + sw128(row, (ch & 3) * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sm.full[s]));
+        mbar_arrive(smem_u32(&sm.raw_empty[r]));
+      }
+      if (it & 1) W.next(P);
+    }
+  } else if (warp == kPxWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t id_s = umma_idesc_bf16(kPxRows, kPxTile);
+    const uint32_t id_o = umma_idesc_bf16_bmn(kPxRows, kHeadDim);
+    const uint32_t qs = smem_u32(sm.q), ring = smem_u32(sm.ring);
+    asm volatile("bar.sync 1, 288;" ::: "memory");     // Q and O are ready
+    tc_fence_after();
+    int lo[2] = {}, hi[2] = {};                        // lanes of each block in tile it - 1
+    int done_s[2] = {0, 0};                            // products S issued
+    for (int it = 0; it <= n; ++it) {
+      const int tk = 2 * it, tv = 2 * it - 1;          // ring positions of K_it and V_(it - 1)
+      if (it < n && !px_wait(P, sm.abort_flag, &sm.full[tk % C::kSlots], (tk / C::kSlots) & 1)) break;
+      if (it >= 1 && !px_wait(P, sm.abort_flag, &sm.full[tv % C::kSlots], (tv / C::kSlots) & 1)) break;
+      const uint32_t ks = ring + (tk % C::kSlots) * kPxTileBytes;
+      const uint32_t vs = ring + (it >= 1 ? tv % C::kSlots : 0) * kPxTileBytes;
+      bool ok = true;
+#pragma unroll
+      for (int g2 = 0; g2 < 2; ++g2) {
+        int nlo = 0, nhi = 0;
+        if (it < n && g2 < nb) W.lanes(P, g2, nlo, nhi);
+        if (it >= 1 && hi[g2] > lo[g2]) {   // O_g += P_g . V_(it - 1) on those lanes
+          if (!px_wait(P, sm.abort_flag, &sm.p_full[g2], (done_s[g2] - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            uint32_t off[4];                 // lanes left as they are
+#pragma unroll
+            for (int w = 0; w < 4; ++w) off[w] = ~lane_bits(lo[g2] - 32 * w, hi[g2] - 32 * w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              umma_bf16_ts_lanes(tmem + 256 + g2 * 128, tmem + g2 * 128 + 8 * k,
+                                 umma_desc_sw128_mn(vs + k * 2048, kPxTile * 128, 1024), id_o, off);
+            if (g2 == 1 || hi[1] <= lo[1]) umma_commit(smem_u32(&sm.empty[tv % C::kSlots]));
+          }
+          __syncwarp();
+        }
+        lo[g2] = nlo;
+        hi[g2] = nhi;
+        if (nhi > nlo) {   // S_g = Q_g . K_it^T, over the P_g that the product before has read
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t o = (k >> 2) * (kPxTile * 128) + (k & 3) * 32;
+              umma_bf16(tmem + g2 * 128, umma_desc_sw128(qs + g2 * (kPxRows * 256) + o, 1024),
+                        umma_desc_sw128(ks + o, 1024), id_s, k > 0);
+            }
+            umma_commit(smem_u32(&sm.s_full[g2]));
+          }
+          __syncwarp();
+          ++done_s[g2];
+        }
+      }
+      if (!ok) break;
+      if (it < n) {
+        if (lane == 0) umma_commit(smem_u32(&sm.empty[tk % C::kSlots]));
+        __syncwarp();
+        W.next(P);
+      }
+    }
+    if (lane == 0) {   // every issued product has landed before TMEM is read or released
+      umma_commit(smem_u32(&sm.done[0]));
+      if (!mbar_wait(smem_u32(&sm.done[0]), 0)) {
+        record_status(P.status, kStatusTimeout);
+        *sm.abort_flag = 1;
+      }
+    }
+    __syncwarp();
+  }
+  const int64_t row = row0 + g * kPxRows + (warp & 3) * 32 + lane;   // softmax warps: the thread's row
+  if (warp < 8 && g < nb) {
+    // ------------------------------------------------------------ softmax
+    const uint32_t s_addr = lane_addr + g * 128, o_addr = lane_addr + 256 + g * 128;
+    const float sc = P.scale_log2;
+    const float2 sc2 = make_float2(sc, sc);
+    const int rl = (warp & 3) * 32 + lane;
+    const int my_q = (int)(row / P.n_heads);           // flat query token
+    int c_s = 0;                                       // tiles that concerned this block
+    for (int it = 0; it < n; ++it) {
+      int lo, hi;
+      W.lanes(P, g, lo, hi);
+      const bool own = W.own(P);
+      const int tile_valid = W.valid(P);
+      int valid = tile_valid;
+      if (own) valid = (rl >= lo && rl < hi) ? P.seq.len[W.b] - P.n_q + (my_q - W.b * P.n_q) + 1 - W.j * kPxTile : 0;
+      W.next(P);
+      const float *ksc = sm.scale, *vsc = sm.scale;
+      if constexpr (C::kFp8) {
+        const int tk = 2 * it, tv = 2 * it + 1;
+        if (!px_wait(P, sm.abort_flag, &sm.sc_full[tk % C::kScaleSlots], (tk / C::kScaleSlots) & 1)) break;
+        if (!px_wait(P, sm.abort_flag, &sm.sc_full[tv % C::kScaleSlots], (tv / C::kScaleSlots) & 1)) break;
+        ksc += (tk % C::kScaleSlots) * kPxTile;
+        vsc += (tv % C::kScaleSlots) * kPxTile;
+      }
+      if (hi > lo) {
+        if (!px_wait(P, sm.abort_flag, &sm.s_full[g], c_s & 1)) break;
+        tc_fence_after();
+        if (own && !C::kFp8 && tile_valid < kPxTile) {   // V rows behind the sequence's last: zero
+          const int tv = 2 * it + 1;
+          if (!px_wait(P, sm.abort_flag, &sm.full[tv % C::kSlots], (tv / C::kSlots) & 1)) break;
+          uint8_t *vt = sm.ring + (tv % C::kSlots) * kPxTileBytes;
+          for (int e = tile_valid * 16 + (threadIdx.x & 127); e < kPxTile * 16; e += 128)
+            *reinterpret_cast<uint4 *>(vt + (e & 1) * (kPxTile * 128) + (e >> 1) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        if (lo < (warp & 3) * 32 + 32 && hi > (warp & 3) * 32) {   // some lane of this warp
+          // the row maximum; the scores stay in TMEM and are read again below
+          float mt = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            float x[32];
+            px_scores<C::kFp8>(s_addr + c, ksc + c, valid - c, x);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mt = fmax3(mt, x[i], x[i + 1]);
+          }
+          mt *= sc;
+          const bool move = mt > m_run + kPxLazy;
+          if (__any_sync(0xffffffffu, move)) {
+            const float m_new = move ? mt : m_run;
+            const float alpha = move ? (m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new)) : 1.f;
+            l_run *= alpha;
+            m_run = m_new;
+            if (c_s > 0) {   // rescale this row of O (S has landed, and so the products before it)
+#pragma unroll 1
+              for (int c = 0; c < 128; c += 32) {
+                float v[32];
+                tmem_ld32(o_addr + c, v);
+                tmem_wait_ld();
+                uint32_t u[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * alpha);
+                tmem_st32(o_addr + c, u);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float mref = (m_run == -INFINITY) ? 0.f : m_run;
+          const float2 neg = make_float2(-mref, -mref);
+          float2 ls = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            float x[32];
+            px_scores<C::kFp8>(s_addr + c, ksc + c, valid - c, x);
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 z = ffma2(make_float2(x[2 * k], x[2 * k + 1]), sc2, neg);
+              float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+              ls = fadd2(ls, e);
+              if (C::kFp8) e = fmul2(e, *reinterpret_cast<const float2 *>(vsc + c + 2 * k));
+              pk[k] = pack_bf16(e.x, e.y);
+            }
+            tmem_st16(s_addr + c / 2, pk);   // columns that have been read
+          }
+          l_run += ls.x + ls.y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[g]));
+        ++c_s;
+      }
+      if constexpr (C::kFp8) {
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.sc_empty[(2 * it) % C::kScaleSlots]));
+          mbar_arrive(smem_u32(&sm.sc_empty[(2 * it + 1) % C::kScaleSlots]));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();   // the MMA warp has seen every product land
+  tc_fence_after();
+  const bool aborted = *sm.abort_flag != 0;
+  if (warp < 8 && g < nb && !aborted) {
+    // ------------------------------------------------------------ O and log-sum-exp
+    const bool some = m_run != -INFINITY || l_run != 0.f;   // a row may see nothing in this range
+    const float inv = some ? 1.f / l_run : 0.f;
+    const bool whole = P.n_splits == 1;
+    float *part = P.part_o + ((int64_t)split * P.rows + row) * kHeadDim;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float v[32];
+      tmem_ld32(lane_addr + 256 + g * 128 + c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= inv;
+      if (row >= P.rows) continue;
+      if (!whole || P.out_f32) {
+        float *o = whole ? static_cast<float *>(P.out) + row * kHeadDim : part;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<float4 *>(o + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(P.out) + row * kHeadDim;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          *reinterpret_cast<uint4 *>(o + c + i) =
+              make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
+                         pack_bf16(v[i + 6], v[i + 7]));
+      }
+    }
+    const float lse = some ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+    if (row < P.rows) {
+      if (!whole) P.part_lse[(int64_t)split * P.rows + row] = lse;
+      else if (P.lse) P.lse[row] = lse;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPxWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kPxCols);
+  }
+}
+
+// out = sum_j w_j O_j / sum_j w_j, w_j = exp(lse_j - max lse), over the ranges of a row's tiles. One
+// CTA per row: each of its warps sums every kPmWarps-th part, four columns per lane, and the warps'
+// sums meet in shared memory, in warp order.
+constexpr int kPmWarps = 4;
+
+__global__ void __launch_bounds__(kPmWarps * 32) prefix_merge_kernel(const __grid_constant__ PrefixParams P) {
+  __shared__ float4 s_o[kPmWarps][32];
+  __shared__ float s_l[kPmWarps];
+  __shared__ float s_w[kPxMaxSplits];
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_launch_dependents();
+  griddep_wait();
+  // every warp finds the maximum itself; warp 0 leaves the parts' log-sum-exps in shared memory
+  float M = -INFINITY;
+  for (int j = lane; j < P.n_splits; j += 32) {
+    const float l = P.part_lse[j * P.rows + row];
+    if (warp == 0) s_w[j] = l;
+    M = fmaxf(M, l);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float ref = M == -INFINITY ? 0.f : M;
+  __syncthreads();
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int j = warp; j < P.n_splits; j += kPmWarps) {
+    const float w = expf(s_w[j] - ref);
+    const float4 v = *reinterpret_cast<const float4 *>(P.part_o + (j * P.rows + row) * kHeadDim + lane * 4);
+    L += w;
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  s_o[warp][lane] = o;
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int i = 1; i < kPmWarps; ++i) {
+    const float4 v = s_o[i][lane];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
+    L += s_l[i];
+  }
+  const float inv = 1.f / L;
+  const int64_t at = row * kHeadDim + lane * 4;
+  if (P.out_f32)
+    *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(P.out) + at) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (P.lse && lane == 0) P.lse[row] = M + logf(L);
+}
+
+template <int KV>
+cudaError_t launch_px(const PrefixMaps &tm, const PrefixParams &p, cudaStream_t s) {
+  using C = PxCfg<KV>;
+  auto kern = prefix_attn_kernel<KV>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, p.n_pairs * p.n_splits, C::kThreads, C::kBytes, s, tm, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_attn(int kv_dtype, const PrefixMaps &tm, const PrefixParams &p, cudaStream_t s) {
+  return kv_dtype == HS2_KV_BF16 ? launch_px<kKvBf16>(tm, p, s) : launch_px<kKvFp8>(tm, p, s);
+}
+
+cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s) {
+  return launch_pdl(prefix_merge_kernel, (int)p.rows, kPmWarps * 32, 0, s, p);
+}
+
+}  // namespace hs2

@@ -1567,6 +1567,139 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
   return st == HS2_OK ? ok() : st;
 }
 
+// ------------------------------------------------------------------ shared prefix
+
+namespace {
+constexpr int kPrefixTile = 128;          // prefix rows per tile, and (query, head) rows per block
+constexpr int kPrefixCtas = 148;          // one CTA per SM
+
+// Work split and workspace of hs2_prefix_attn.
+struct PrefixPlan {
+  int64_t rows = 0;
+  int n_tiles = 0, n_pairs = 0, n_splits = 1;
+  size_t off_part_o = 0, off_part_lse = 0, total = 0;
+};
+
+// Every pair of row blocks walks its tiles (the prefix's and its sequences' own) in n_splits
+// ranges. Fewer ranges mean fewer partial results, more fill the last wave of CTAs better: the
+// count with the least time, a CTA costing its tiles and about six tiles' time more (set-up, first
+// loads, the result).
+PrefixPlan prefix_plan(const hs2_kv_view *kv, int32_t prefix_len) {
+  PrefixPlan F;
+  const int64_t per_seq = (int64_t)kv->n_q * kv->n_heads;
+  F.rows = kv->batch * per_seq;
+  F.n_tiles = (prefix_len + kPrefixTile - 1) / kPrefixTile;
+  F.n_pairs = (int)((F.rows + 2 * kPrefixTile - 1) / (2 * kPrefixTile));
+  // own tiles: of all sequences, over the pairs that hold their rows (at least one pair each)
+  int64_t own = 0;
+  for (int b = 0; b < kv->batch; ++b) {
+    const int64_t pairs = ((b + 1) * per_seq - 1) / (2 * kPrefixTile) - b * per_seq / (2 * kPrefixTile) + 1;
+    own += pairs * ((kv->kv_len[b] + kPrefixTile - 1) / kPrefixTile);
+  }
+  const int64_t tiles = F.n_tiles + (own + F.n_pairs - 1) / F.n_pairs;   // of a pair, on average
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= (int)std::min<int64_t>(kPxMaxSplits, tiles); ++s) {
+    const int64_t waves = ((int64_t)F.n_pairs * s + kPrefixCtas - 1) / kPrefixCtas;
+    const int64_t cost = waves * ((tiles + s - 1) / s + 6);
+    if (cost < best) {
+      best = cost;
+      F.n_splits = s;
+    }
+  }
+  size_t o = kAlign;   // the status word
+  F.off_part_o = o;
+  if (F.n_splits > 1) o = align_up(o + (size_t)F.n_splits * F.rows * kHeadDim * 4);
+  F.off_part_lse = o;
+  if (F.n_splits > 1) o = align_up(o + (size_t)F.n_splits * F.rows * 4);
+  F.total = o;
+  return F;
+}
+
+hs2_status check_prefix(const hs2_kv_view *kv, int32_t prefix_len) {
+  hs2_status st = validate_view(kv);
+  if (st != HS2_OK) return st;
+  if (prefix_len < 0 || prefix_len > kv->kv_rows)
+    return fail(HS2_ERR_INVALID_ARG, "prefix_len %d outside [0, %lld]", prefix_len, (long long)kv->kv_rows);
+  if ((int64_t)kv->batch * kv->n_q * kv->n_heads > INT32_MAX)
+    return fail(HS2_ERR_UNSUPPORTED, "too many query rows");
+  return HS2_OK;
+}
+}  // namespace
+
+hs2_status hs2_prefix_attn_workspace_size(const hs2_kv_view *kv, int32_t prefix_len, size_t *bytes) {
+  hs2_status st = check_prefix(kv, prefix_len);
+  if (st != HS2_OK) return st;
+  if (!bytes) return fail(HS2_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = prefix_plan(kv, prefix_len).total;
+  return ok();
+}
+
+hs2_status hs2_prefix_attn(const hs2_kv_view *kv, int64_t prefix_start, int32_t prefix_len,
+                           const void *q, float softmax_scale, void *out, int32_t out_dtype,
+                           float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+  hs2_status st = check_prefix(kv, prefix_len);
+  if (st != HS2_OK) return st;
+  if (prefix_start < 0 || prefix_start > kv->kv_rows - prefix_len)
+    return fail(HS2_ERR_INVALID_ARG, "prefix rows [%lld, %lld) outside [0, %lld)", (long long)prefix_start,
+                (long long)(prefix_start + prefix_len), (long long)kv->kv_rows);
+  if (!q || !out) return fail(HS2_ERR_INVALID_ARG, "q / out is NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(HS2_ERR_INVALID_ARG, "q / out must be 16-byte aligned");
+  if (!valid_scale(softmax_scale)) return fail(HS2_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  if (!out_type(out_dtype)) return fail(HS2_ERR_INVALID_ARG, "out_dtype %d", out_dtype);
+  const PrefixPlan F = prefix_plan(kv, prefix_len);
+  if (!workspace) return fail(HS2_ERR_INVALID_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign)
+    return fail(HS2_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (workspace_bytes < F.total)
+    return fail(HS2_ERR_WORKSPACE, "workspace %zu bytes < %zu required (hs2_prefix_attn_workspace_size)",
+                workspace_bytes, F.total);
+  if ((st = get_encoder()) != HS2_OK) return st;
+  PrefixMaps pm;
+  memset(&pm, 0, sizeof pm);
+  const bool bf16 = kv->kv_dtype == HS2_KV_BF16;
+  const int row_bytes = bf16 ? 256 : 128;
+  for (int i = 0; i < 4; ++i) {
+    // the prefix's maps end at its last row: what lies behind reads as zero
+    const bool own = i >= 2;
+    const uint8_t *base = static_cast<const uint8_t *>(i & 1 ? kv->v : kv->k);
+    const int64_t rows = own ? kv->kv_rows : prefix_len;
+    if (rows == 0) continue;
+    st = encode_2d(i == 0 ? &pm.pk : i == 1 ? &pm.pv : i == 2 ? &pm.k : &pm.v,
+                   bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, bf16 ? 2 : 1,
+                   own ? base : base + prefix_start * row_bytes, rows, 128, 128, kPrefixTile, bf16 ? 64 : 128,
+                   bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, own ? "K/V" : "prefix K/V");
+    if (st != HS2_OK) return st;
+  }
+  PrefixParams pp;
+  memset(&pp, 0, sizeof pp);
+  for (int b = 0; b < kv->batch; ++b) {
+    pp.seq.start[b] = kv->kv_start[b];
+    pp.seq.len[b] = kv->kv_len[b];
+  }
+  pp.n_q = kv->n_q;
+  pp.n_heads = kv->n_heads;
+  pp.rows = F.rows;
+  pp.prefix_start = prefix_start;
+  pp.prefix_len = prefix_len;
+  pp.n_tiles = F.n_tiles;
+  pp.n_pairs = F.n_pairs;
+  pp.n_splits = F.n_splits;
+  pp.scale_log2 = softmax_scale * 1.4426950408889634f;
+  pp.q = q;
+  pp.k_scale = kv->k_scale;
+  pp.v_scale = kv->v_scale;
+  pp.part_o = ws_at<float>(workspace, F.off_part_o);
+  pp.part_lse = ws_at<float>(workspace, F.off_part_lse);
+  pp.out = out;
+  pp.out_f32 = out_dtype == HS2_OUT_F32;
+  pp.lse = lse;
+  pp.status = static_cast<uint32_t *>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = cuda_check(launch_prefix_attn(kv->kv_dtype, pm, pp, s), "prefix attention");
+  if (st == HS2_OK && F.n_splits > 1) st = cuda_check(launch_prefix_merge(pp, s), "prefix merge");
+  return st == HS2_OK ? ok() : st;
+}
+
 hs2_status hs2_selftest_wait_timeout(uint32_t limit_us, void *workspace, size_t workspace_bytes,
                                      void *stream) {
   if (limit_us < 1 || limit_us > 2000000) return fail(HS2_ERR_INVALID_ARG, "limit_us %u outside [1, 2e6]", limit_us);

@@ -198,6 +198,31 @@ struct GemmMaps {
 // tokens per tile: 32, 64 or 128; a tile is 128 output features x that many tokens
 cudaError_t launch_gemm_fp8_tokens(int tokens, const GemmMaps &tm, const GemmParams &p, cudaStream_t s);
 
+// Attention of a batch whose sequences share a prefix.
+constexpr int kPxMaxSplits = 148;   // ranges of a row's tiles, at most
+struct PrefixParams {
+  SeqTable seq;               // start, len: the sequences' own rows
+  int32_t n_q, n_heads;
+  int64_t rows;               // B * n_q * H
+  int64_t prefix_start;
+  int32_t prefix_len, n_tiles;   // prefix rows, and 128-row tiles of them
+  int32_t n_pairs, n_splits;  // pairs of 128-row blocks; contiguous ranges of a pair's tiles
+  float scale_log2;
+  const void *q;              // bf16 [rows, 128]
+  const float *k_scale, *v_scale;   // e4m3
+  float *part_o, *part_lse;   // n_splits > 1: [n_splits, rows, 128], [n_splits, rows]
+  void *out;
+  int32_t out_f32;
+  float *lse;                 // or null
+  uint32_t *status;           // cleared by the first CTA
+};
+struct PrefixMaps {
+  CUtensorMap pk, pv;         // the prefix's rows alone; boxes of 128 rows x 128 bytes
+  CUtensorMap k, v;           // the whole cache
+};
+cudaError_t launch_prefix_attn(int kv_dtype, const PrefixMaps &tm, const PrefixParams &p, cudaStream_t s);
+cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s);
+
 // Largest thread-block cluster the sparse layer may use for this cache type and head count.
 int sparse_max_cluster(int kv_dtype, int n_heads);
 
