@@ -52,7 +52,8 @@ def check(out, a, sa, w, sw):
 
 SHAPES = [(1, 1, 16), (1, 256, 4096), (2, 129, 128), (7, 128, 144), (8, 1000, 4112), (31, 4096, 512), (32, 130, 272),
           (33, 640, 2048), (64, 64, 1024), (65, 257, 4096), (127, 384, 1040), (128, 128, 128), (129, 8, 640), (200, 1000, 2064),
-          (300, 520, 16384), (1024, 256, 272), (777, 1000, 2064), (2500, 1280, 400), (1, 4096, 65536)]
+          (300, 520, 16384), (1024, 256, 272), (777, 1000, 2064), (2500, 1280, 400), (1, 4096, 65536),
+          (9473, 100, 2064), (5000, 333, 272), (1300, 2000, 1040), (20000, 256, 16), (2049, 2305, 4112)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -77,7 +78,7 @@ def test_product(m, n, k, dtype):
 def test_aligned_wide_stores_and_row_strides():
     """Output rows that allow wide stores (n not a multiple of a piece) and ones that do not."""
     g = torch.Generator().manual_seed(11)
-    for m, n in ((300, 1000), (260, 999), (40, 1004), (1500, 333)):
+    for m, n in ((300, 1000), (260, 999), (40, 1004), (1500, 333), (4900, 1001), (5000, 1000)):
         a, w = codes_of(m, 512, g), codes_of(n, 512, g)
         sa, sw = scales_of(4, m, g), scales_of(4, -(-n // 128), g)
         first = None

@@ -1,0 +1,331 @@
+// gemm_fp8_pair.cu -- the e4m3 product with block scales for many tokens: 256 x 256 tiles of the
+// result, each by a pair of CTAs (a cluster of two on neighbouring SMs, tcgen05 cta_group::2).
+//
+// A CTA of the pair holds 128 tokens' codes and 128 output features' codes of each 128-wide
+// block along k (32 KB per stage): the pair's product of 256 x 256 reads each byte from L2 once
+// per 256 rows of the other operand, which the e4m3 rate needs (a 128 x 128 tile would ask L2
+// for twice the bytes). Its accumulator is 256 TMEM columns in each CTA, tokens on the lanes; two of
+// them alternate. The scales change with every block, so the epilogue warps read each block's
+// accumulator, scale it (one factor per thread: a token's scale times its 128 features') and add it
+// to float32 sums in registers, while the tensor cores work on the next block.
+//   warp 9      TMA producer of its CTA's stages; bytes of both CTAs complete on the leader's barrier
+//   warp 8      TMEM owner; in the leader (rank 0) also the MMA issuer for both
+//   warps 0..7  epilogue: warp w has lanes 32 (w % 4) .. + 31 and features 128 (w / 4) .. + 127
+// Persistent over the tiles, features fastest: the CTAs at work share a few token tiles and the
+// weights, which stay in L2. Results pass through shared memory, a 4 KB square per warp, so that
+// rows are stored in 128-byte pieces.
+#include "common.cuh"
+#include "internal.h"
+#include "tc05.cuh"
+
+namespace hs2 {
+
+namespace {
+
+constexpr int kGpWarpMma = 8, kGpWarpTma = 9, kGpThreads = 10 * 32;
+constexpr int kGpTile = 256;
+constexpr int kGpHalf = 128 * 128;               // a CTA's codes of one operand and block
+constexpr int kGpStageBytes = 2 * kGpHalf;
+constexpr int kGpStages = 6;
+constexpr int kGpOutBytes = 4096;                // per epilogue warp: 32 rows x 128 bytes
+constexpr size_t kGpBytes = 1024 + (size_t)kGpStages * kGpStageBytes + 8 * kGpOutBytes + (2 * kGpStages + 5) * 8 + 16;
+static_assert(kGpBytes <= 227 * 1024, "shared memory");
+
+struct GpSmem {
+  uint8_t *stages, *out;
+  uint64_t *full, *empty, *acc_full, *acc_empty, *done;
+  uint32_t *tmem_base;
+  volatile int *abort_flag;
+  __device__ explicit GpSmem(uint8_t *raw) {
+    stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    out = stages + kGpStages * kGpStageBytes;
+    full = reinterpret_cast<uint64_t *>(out + 8 * kGpOutBytes);
+    empty = full + kGpStages;
+    acc_full = empty + kGpStages;
+    acc_empty = acc_full + 2;
+    done = acc_empty + 2;
+    tmem_base = reinterpret_cast<uint32_t *>(done + 1);
+    abort_flag = reinterpret_cast<volatile int *>(tmem_base + 1);
+  }
+};
+
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+// 2-D tile load of a CTA pair: into this CTA's memory, completing on a barrier of either CTA
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t cluster_bar,
+                                                 int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate));
+}
+
+// Arrives once on the barrier at this offset in both CTAs when the pair's products so far are done.
+__device__ __forceinline__ void umma_commit_pair(uint32_t mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ bool gp_wait(uint32_t *status, volatile int *abort_flag, uint64_t *bar, uint32_t parity) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    ok = mbar_wait(smem_u32(bar), parity);
+    if (!ok) {
+      record_status(status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    if (*abort_flag) ok = false;
+  }
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// One warp's 32 rows x 128 bytes through its square of shared memory: lane = row writes its 8
+// pieces of 16 bytes (swizzled), then each row leaves by 8 neighbouring lanes. `cols`: elements of
+// the row that exist.
+template <class T>
+__device__ __forceinline__ void store_square(uint8_t *sq, const uint4 (&v)[8], T *out, int64_t ldo, int rows, int cols,
+                                             bool wide) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(sq + sw128(lane, c * 16)) = v[c];
+  __syncwarp();
+  constexpr int per = 16 / sizeof(T);
+  if (wide) {
+    const int c = lane & 7;
+#pragma unroll
+    for (int r = lane >> 3; r < 32; r += 4)
+      if (r < rows) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(sq + sw128(r, c * 16));
+        T *o = out + r * ldo + c * per;
+        if ((c + 1) * per <= cols) {
+          *reinterpret_cast<uint4 *>(o) = u;
+        } else {
+          const T *e = reinterpret_cast<const T *>(&u);
+#pragma unroll
+          for (int i = 0; i < per; ++i)
+            if (c * per + i < cols) o[i] = e[i];
+        }
+      }
+  } else {
+    for (int r = 0; r < min(rows, 32); ++r)
+      for (int c = lane; c < min(cols, 8 * per); c += 32)
+        out[r * ldo + c] = *reinterpret_cast<const T *>(sq + sw128(r, c * (int)sizeof(T)));
+  }
+}
+
+__global__ void __launch_bounds__(kGpThreads, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__ GemmParams P) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  GpSmem sm(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;                 // in the pair
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  const int n_tiles = P.n_tiles * P.m_tiles, kb = P.kb;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGpStages; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&sm.acc_full[a]), 1);
+      mbar_init(smem_u32(&sm.acc_empty[a]), 16);   // the epilogue warps of both CTAs
+    }
+    mbar_init(smem_u32(&sm.done[0]), 1);
+    *sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kGpWarpTma && lane == 0) {
+    prefetch_tensormap(&tm.a);
+    prefetch_tensormap(&tm.w);
+  }
+  if (warp == kGpWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(sm.tmem_base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem_base;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
+
+  if (warp == kGpWarpTma) {
+    // ------------------------------------------------------------ producer
+    int it = 0;
+    bool ok = true;
+    for (int tile = first; tile < n_tiles && ok; tile += stride) {
+      const int nt = tile % P.n_tiles, mt = tile / P.n_tiles;
+      for (int b = 0; b < kb; ++b, ++it) {
+        const int s = it % kGpStages;
+        if (it >= kGpStages && !gp_wait(P.status, sm.abort_flag, &sm.empty[s], ((it / kGpStages) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t st = smem_u32(sm.stages + s * kGpStageBytes);
+          const uint32_t bar = map_rank(smem_u32(&sm.full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sm.full[s]), 2 * kGpStageBytes);
+          tma_load_2d_pair(st, &tm.a, bar, b * 128, mt * kGpTile + rank * 128);
+          tma_load_2d_pair(st + kGpHalf, &tm.w, bar, b * 128, nt * kGpTile + rank * 128);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) {   // gave up: copies in flight land before the CTA ends (they take microseconds)
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000ull) {}
+    }
+    __syncwarp();
+  } else if (warp == kGpWarpMma && rank == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t idesc = umma_idesc_e4m3(kGpTile, kGpTile);
+    int it = 0;
+    bool ok = true;
+    for (int tile = first; tile < n_tiles && ok; tile += stride) {
+      for (int b = 0; b < kb; ++b, ++it) {
+        const int s = it % kGpStages, a = it & 1;
+        if ((it >= 2 && !gp_wait(P.status, sm.abort_flag, &sm.acc_empty[a], ((it >> 1) & 1) ^ 1)) ||
+            !gp_wait(P.status, sm.abort_flag, &sm.full[s], (it / kGpStages) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t st = smem_u32(sm.stages + s * kGpStageBytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_e4m3_pair(tmem + a * 256, umma_desc_sw128(st + k * 32, 1024), umma_desc_sw128(st + kGpHalf + k * 32, 1024),
+                           idesc, k != 0);
+          umma_commit_pair(smem_u32(&sm.empty[s]));
+          umma_commit_pair(smem_u32(&sm.acc_full[a]));
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {   // every product has landed before TMEM is released
+      umma_commit_pair(smem_u32(&sm.done[0]));
+      if (!mbar_wait(smem_u32(&sm.done[0]), 0)) {
+        record_status(P.status, kStatusTimeout);
+        *sm.abort_flag = 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
+    const uint32_t freed[2] = {map_rank(smem_u32(&sm.acc_empty[0]), 0), map_rank(smem_u32(&sm.acc_empty[1]), 0)};
+    uint8_t *sq = sm.out + warp * kGpOutBytes;
+    const bool wide = (P.ldo * (P.out_f32 ? 4 : 2)) % 16 == 0 && (reinterpret_cast<uintptr_t>(P.out) & 15) == 0;
+    int it = 0;
+    bool ok = true;
+    for (int tile = first; tile < n_tiles && ok; tile += stride) {
+      const int nt = tile % P.n_tiles, mt = tile / P.n_tiles;
+      const int m0 = mt * kGpTile + rank * 128 + quad * 32, n0 = nt * kGpTile + half * 128;
+      // scales: this token's, and the features' (clamped where neither exists)
+      const float *sa = P.a_scale + min(m0 + lane, P.m - 1);
+      const float *sw = P.w_scale + min(n0, P.n - 1) / 128;
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+      float s0 = sa[0] * sw[0], s1 = kb > 1 ? sa[P.a_scale_ld] * sw[P.w_scale_ld] : 0.f;
+      for (int b = 0; b < kb; ++b, ++it) {
+        const int a = it & 1;
+        float s2 = 0.f;
+        if (b + 2 < kb) s2 = sa[(b + 2) * P.a_scale_ld] * sw[(b + 2) * P.w_scale_ld];
+        if (!gp_wait(P.status, sm.abort_flag, &sm.acc_full[a], (it >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float2 sc = make_float2(s0, s0);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          float v[32];
+          tmem_ld32(lane_addr + a * 256 + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c / 2 + j] = ffma2(make_float2(v[2 * j], v[2 * j + 1]), sc, acc[c / 2 + j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(freed[a]);
+        s0 = s1;
+        s1 = s2;
+      }
+      if (!ok) break;
+      const int rows = P.m - m0, cols = P.n - n0;
+      if (rows <= 0 || cols <= 0) continue;
+      if (P.out_f32) {
+        float *o = static_cast<float *>(P.out) + (int64_t)m0 * P.ldo + n0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4 v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2 x = acc[q * 16 + 2 * c], y = acc[q * 16 + 2 * c + 1];
+            v[c] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+          }
+          if (cols > q * 32) store_square<float>(sq, v, o + q * 32, P.ldo, rows, cols - q * 32, wide);
+        }
+      } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(P.out) + (int64_t)m0 * P.ldo + n0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint4 v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2 *x = acc + q * 32 + 4 * c;
+            v[c] = make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y),
+                              pack_bf16(x[3].x, x[3].y));
+          }
+          if (cols > q * 64) store_square<__nv_bfloat16>(sq, v, o + q * 64, P.ldo, rows, cols - q * 64, wide);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // the pair's products and copies are over in both CTAs
+  if (warp == kGpWarpMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8_pair(const GemmMaps &tm, const GemmParams &p, int pairs, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGpBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(gemm_fp8_pair_kernel, 2 * pairs, kGpThreads, kGpBytes, 2, s, tm, p);
+}
+
+}  // namespace hs2

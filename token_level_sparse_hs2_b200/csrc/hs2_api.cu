@@ -1550,17 +1550,26 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
   gp.out_f32 = out_dtype == HS2_OUT_F32;
   gp.ldo = ldo;
   gp.status = static_cast<uint32_t *>(workspace);
-  const int tokens = m <= 32 ? 32 : m <= 64 ? 64 : 128;
-  gp.n_tiles = (n + 127) / 128;
-  gp.m_tiles = (int32_t)((m + tokens - 1) / tokens);
+  // pairs of CTAs with 256 x 256 tiles once these fill half the chip
+  const int64_t big = (int64_t)((n + 255) / 256) * ((m + 255) / 256);
+  const bool pair = big >= sms / 4;
+  const int tokens = pair ? 128 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  gp.n_tiles = pair ? (n + 255) / 256 : (n + 127) / 128;
+  gp.m_tiles = pair ? (int32_t)((m + 255) / 256) : (int32_t)((m + tokens - 1) / tokens);
   const int64_t tiles = (int64_t)gp.n_tiles * gp.m_tiles;
-  gp.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, gp.kb, sms / std::max<int64_t>(1, tiles)}));
+  gp.split = pair ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({8, gp.kb, sms / std::max<int64_t>(1, tiles)}));
   if (tiles * gp.split > INT32_MAX) return fail(HS2_ERR_UNSUPPORTED, "too many output tiles");
   GemmMaps tm;
+  memset(&tm, 0, sizeof tm);
   if ((st = encode_2d(&tm.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, m, k, lda, tokens, 128,
                       CU_TENSOR_MAP_SWIZZLE_128B, "a")) != HS2_OK) return st;
   if ((st = encode_2d(&tm.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, n, k, ldw, 128, 128,
                       CU_TENSOR_MAP_SWIZZLE_128B, "w")) != HS2_OK) return st;
+  if (pair) {
+    st = cuda_check(launch_gemm_fp8_pair(tm, gp, (int)std::min<int64_t>(tiles, sms / 2), static_cast<cudaStream_t>(stream)),
+                    "fp8 product");
+    return st == HS2_OK ? ok() : st;
+  }
   if ((st = encode_2d(&tm.sa, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a_scale, gp.kb, m, a_scale_ld, 1,
                       tokens, CU_TENSOR_MAP_SWIZZLE_NONE, "a_scale")) != HS2_OK) return st;
   st = cuda_check(launch_gemm_fp8_tokens(tokens, tm, gp, static_cast<cudaStream_t>(stream)), "fp8 product");

@@ -197,6 +197,8 @@ struct GemmMaps {
 };
 // tokens per tile: 32, 64 or 128; a tile is 128 output features x that many tokens
 cudaError_t launch_gemm_fp8_tokens(int tokens, const GemmMaps &tm, const GemmParams &p, cudaStream_t s);
+// 256 x 256 tiles, `pairs` clusters of two CTAs (maps with boxes of 128 rows; sa unused)
+cudaError_t launch_gemm_fp8_pair(const GemmMaps &tm, const GemmParams &p, int pairs, cudaStream_t s);
 
 // Attention of a batch whose sequences share a prefix.
 constexpr int kPxMaxSplits = 148;   // ranges of a row's tiles, at most
