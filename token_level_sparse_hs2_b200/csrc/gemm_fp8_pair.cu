@@ -10,6 +10,7 @@
 // to float32 sums in registers, while the tensor cores work on the next block.
 //   warp 9      TMA producer of its CTA's stages; bytes of both CTAs complete on the leader's barrier
 //   warp 8      TMEM owner; in the leader (rank 0) also the MMA issuer for both
+//   warps 10, 11  nothing (the register split goes by groups of four warps)
 //   warps 0..7  epilogue: warp w has lanes 32 (w % 4) .. + 31 and features 128 (w / 4) .. + 127
 // Persistent over the tiles, features fastest: the CTAs at work share a few token tiles and the
 // weights, which stay in L2. Results pass through shared memory, a 4 KB square per warp, so that
@@ -22,7 +23,10 @@ namespace hs2 {
 
 namespace {
 
-constexpr int kGpWarpMma = 8, kGpWarpTma = 9, kGpThreads = 10 * 32;
+constexpr int kGpWarpMma = 8, kGpWarpTma = 9, kGpThreads = 12 * 32;
+// Registers: 384 threads x 168 at launch = 64,512 = 256 epilogue threads x 216 + 128 others x 72.
+constexpr int kGpRegsEpilogue = 216, kGpRegsOther = 72;
+static_assert(256 * kGpRegsEpilogue + 128 * kGpRegsOther <= kGpThreads * 168, "register split");
 constexpr int kGpTile = 256;
 constexpr int kGpHalf = 128 * 128;               // a CTA's codes of one operand and block
 constexpr int kGpStageBytes = 2 * kGpHalf;
@@ -81,25 +85,40 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t mbar) {
       : "memory");
 }
 
+// Relaxed: what the arrival hands over is tensor memory, ordered by the tcgen05 fence before it; a
+// release at cluster scope would wait for the thread's global loads (1247 -> see below).
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ bool gp_wait(uint32_t *status, volatile int *abort_flag, uint64_t *bar, uint32_t parity) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) {
-    ok = mbar_wait(smem_u32(bar), parity);
-    if (!ok) {
+// Bounded wait by every calling thread (a warp's lanes test the barrier in one instruction). The
+// usual case, a phase that is complete already, costs one test; a wait that runs out records the
+// timeout, and one of a CTA that gave up elsewhere ends early.
+__device__ __forceinline__ bool gp_wait_slow(uint32_t *status, volatile int *abort_flag, uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)
+      if (mbar_test_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
       record_status(status, kStatusTimeout);
       *abort_flag = 1;
+      return false;
     }
-    if (*abort_flag) ok = false;
   }
-  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+__device__ __forceinline__ bool gp_wait(uint32_t *status, volatile int *abort_flag, uint64_t *bar, uint32_t parity) {
+  const uint32_t b = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_test_wait(b, parity)) return true;
+  return gp_wait_slow(status, abort_flag, b, parity);
 }
 
 // One warp's 32 rows x 128 bytes through its square of shared memory: lane = row writes its 8
@@ -176,60 +195,59 @@ __global__ void __launch_bounds__(kGpThreads, 1)
   griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
 
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGpRegsOther));
   if (warp == kGpWarpTma) {
-    // ------------------------------------------------------------ producer
-    int it = 0;
-    bool ok = true;
-    for (int tile = first; tile < n_tiles && ok; tile += stride) {
-      const int nt = tile % P.n_tiles, mt = tile / P.n_tiles;
-      for (int b = 0; b < kb; ++b, ++it) {
-        const int s = it % kGpStages;
-        if (it >= kGpStages && !gp_wait(P.status, sm.abort_flag, &sm.empty[s], ((it / kGpStages) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
+    // ------------------------------------------------------------ producer (one thread)
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; tile < n_tiles && ok; tile += stride) {
+        const int nt = tile % P.n_tiles, mt = tile / P.n_tiles;
+        for (int b = 0; b < kb; ++b, ++it) {
+          const int s = it % kGpStages;
+          if (it >= kGpStages && !gp_wait(P.status, sm.abort_flag, &sm.empty[s], ((it / kGpStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
           const uint32_t st = smem_u32(sm.stages + s * kGpStageBytes);
           const uint32_t bar = map_rank(smem_u32(&sm.full[s]), 0);
           if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sm.full[s]), 2 * kGpStageBytes);
           tma_load_2d_pair(st, &tm.a, bar, b * 128, mt * kGpTile + rank * 128);
           tma_load_2d_pair(st + kGpHalf, &tm.w, bar, b * 128, nt * kGpTile + rank * 128);
         }
-        __syncwarp();
       }
-    }
-    if (!ok && lane == 0) {   // gave up: copies in flight land before the CTA ends (they take microseconds)
-      const uint64_t t0 = globaltimer();
-      while (globaltimer() - t0 < 1000000ull) {}
+      if (!ok) {   // gave up: copies in flight land before the CTA ends (they take microseconds)
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {}
+      }
     }
     __syncwarp();
   } else if (warp == kGpWarpMma && rank == 0) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t idesc = umma_idesc_e4m3(kGpTile, kGpTile);
-    int it = 0;
-    bool ok = true;
-    for (int tile = first; tile < n_tiles && ok; tile += stride) {
-      for (int b = 0; b < kb; ++b, ++it) {
-        const int s = it % kGpStages, a = it & 1;
-        if ((it >= 2 && !gp_wait(P.status, sm.abort_flag, &sm.acc_empty[a], ((it >> 1) & 1) ^ 1)) ||
-            !gp_wait(P.status, sm.abort_flag, &sm.full[s], (it / kGpStages) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t st = smem_u32(sm.stages + s * kGpStageBytes);
+    // ------------------------------------------------------------ MMA issuer (one thread)
+    if (lane == 0) {
+      const uint32_t idesc = umma_idesc_e4m3(kGpTile, kGpTile);
+      const uint64_t desc0 = umma_desc_sw128(smem_u32(sm.stages), 1024);
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; tile < n_tiles && ok; tile += stride) {
+        for (int b = 0; b < kb; ++b, ++it) {
+          const int s = it % kGpStages, a = it & 1;
+          if (!gp_wait(P.status, sm.abort_flag, &sm.full[s], (it / kGpStages) & 1) ||
+              (it >= 2 && !gp_wait(P.status, sm.abort_flag, &sm.acc_empty[a], ((it >> 1) & 1) ^ 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = desc0 + (uint32_t)(s * (kGpStageBytes >> 4));   // the address field counts 16 bytes
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_e4m3_pair(tmem + a * 256, umma_desc_sw128(st + k * 32, 1024), umma_desc_sw128(st + kGpHalf + k * 32, 1024),
-                           idesc, k != 0);
-          umma_commit_pair(smem_u32(&sm.empty[s]));
+            umma_e4m3_pair(tmem + a * 256, da + 2 * k, da + (kGpHalf >> 4) + 2 * k, idesc, k != 0);
           umma_commit_pair(smem_u32(&sm.acc_full[a]));
+          umma_commit_pair(smem_u32(&sm.empty[s]));
         }
-        __syncwarp();
       }
-    }
-    if (lane == 0) {   // every product has landed before TMEM is released
+      // every product has landed before TMEM is released
       umma_commit_pair(smem_u32(&sm.done[0]));
       if (!mbar_wait(smem_u32(&sm.done[0]), 0)) {
         record_status(P.status, kStatusTimeout);
@@ -237,7 +255,9 @@ __global__ void __launch_bounds__(kGpThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGpRegsEpilogue));
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3, half = warp >> 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
@@ -255,30 +275,53 @@ __global__ void __launch_bounds__(kGpThreads, 1)
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      float s0 = sa[0] * sw[0], s1 = kb > 1 ? sa[P.a_scale_ld] * sw[P.w_scale_ld] : 0.f;
-      for (int b = 0; b < kb; ++b, ++it) {
-        const int a = it & 1;
-        float s2 = 0.f;
-        if (b + 2 < kb) s2 = sa[(b + 2) * P.a_scale_ld] * sw[(b + 2) * P.w_scale_ld];
-        if (!gp_wait(P.status, sm.abort_flag, &sm.acc_full[a], (it >> 1) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float2 sc = make_float2(s0, s0);
+      // four blocks' scales are loaded while the four before are used: a load's register that is
+      // moved, or multiplied, too early waits for L2 (1560 -> see below clocks a block)
+      float fa[4], fw[4], na[4], nw[4];
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          float v[32];
-          tmem_ld32(lane_addr + a * 256 + c, v);
-          tmem_wait_ld();
+      for (int i = 0; i < 4; ++i) {
+        const int b = min(i, kb - 1);
+        fa[i] = sa[b * P.a_scale_ld];
+        fw[i] = sw[b * P.w_scale_ld];
+      }
+      for (int b0 = 0; b0 < kb && ok; b0 += 4) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c / 2 + j] = ffma2(make_float2(v[2 * j], v[2 * j + 1]), sc, acc[c / 2 + j]);
+        for (int i = 0; i < 4; ++i) {
+          const int b = min(b0 + 4 + i, kb - 1);
+          na[i] = sa[b * P.a_scale_ld];
+          nw[i] = sw[b * P.w_scale_ld];
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(freed[a]);
-        s0 = s1;
-        s1 = s2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (b0 + i < kb && ok) {
+            const int a = it & 1;
+            ok = gp_wait(P.status, sm.abort_flag, &sm.acc_full[a], (it >> 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            const float s0 = fa[i] * fw[i];
+            const float2 sc = make_float2(s0, s0);
+            uint32_t v[2][16];   // 16 columns are scaled and added while the next 16 are on their way
+            tmem_ld16_issue(lane_addr + a * 256, v[0]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              tmem_wait_ld16(v[q & 1]);
+              if (q < 7) tmem_ld16_issue(lane_addr + a * 256 + (q + 1) * 16, v[(q + 1) & 1]);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                acc[q * 8 + j] = ffma2(make_float2(__uint_as_float(v[q & 1][2 * j]), __uint_as_float(v[q & 1][2 * j + 1])),
+                                       sc, acc[q * 8 + j]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(freed[a]);
+            ++it;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          fa[i] = na[i];
+          fw[i] = nw[i];
+        }
       }
       if (!ok) break;
       const int rows = P.m - m0, cols = P.n - n0;
