@@ -107,6 +107,13 @@ __device__ __forceinline__ void umma_commit(uint32_t mbar) {
                ::"r"(mbar) : "memory");
 }
 
+// One lane of the converged warp, known to be one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // Whole-warp TMEM allocation: writes the base address to *dst_smem.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
