@@ -103,9 +103,9 @@ class Case:
 
 DECODE = [([1], 1, 16, 1), ([1, 5], 1, 16, 127), ([300, 1, 77], 1, 32, 128), ([64] * 4, 1, 32, 129), ([3] * 5, 1, 32, 1000),
           ([1, 2, 3, 4, 5, 6, 7, 8, 9], 1, 32, 5000), ([17] * 33, 1, 16, 777), ([200] * 8, 1, 32, 4096), ([2] * 128, 1, 32, 300),
-          ([1000, 10], 1, 16, 20011)]
+          ([1000, 10], 1, 16, 20011), ([1100] * 9, 1, 32, 500), ([2000, 3, 1500, 700] * 5, 1, 16, 77), ([3000] * 8, 1, 32, 6000)]
 CHUNKS = [([2], 2, 16, 1), ([5, 9], 5, 16, 130), ([33, 40, 33], 33, 32, 515), ([129, 300], 129, 32, 1000), ([17], 17, 32, 9001),
-          ([700], 513, 16, 250)]
+          ([700], 513, 16, 250), ([1500, 900, 1200], 3, 32, 3000), ([2000, 1000], 70, 16, 140)]
 
 
 @pytest.mark.parametrize("lens,n_q,heads,prefix", DECODE + CHUNKS)

@@ -41,19 +41,19 @@ constexpr int kPxRows = 128;                       // (query, head) rows per blo
 constexpr int kPxTileBytes = kPxTile * 256;        // two [128][128 B] swizzled dim blocks
 constexpr int kPxRawBytes = kPxTile * 128;         // a tile of codes
 constexpr float kPxLazy = 8.f;
-constexpr int kPxWarpMma = 8, kPxWarpTma = 9, kPxWarpWiden = 10;
+constexpr int kPxWarpMma = 8, kPxWarpTma = 10, kPxWarpWiden = 12;   // MMA: a warp per block; 11: nothing
 constexpr uint32_t kPxCols = 512;                  // S/P at 0 and 128, O at 256 and 384
 
 template <int KV>
 struct PxCfg {
   static constexpr bool kFp8 = KV == kKvFp8;
-  static constexpr int kThreads = (kFp8 ? 14 : 10) * 32;
+  static constexpr int kThreads = (kFp8 ? 16 : 12) * 32;
   static constexpr int kSlots = kFp8 ? 4 : 5;      // ring of bf16 tiles: K_0, V_0, K_1, V_1, ...
   static constexpr int kRaw = kFp8 ? 2 : 0;        // ring of code tiles
   static constexpr int kScaleSlots = kFp8 ? 3 : 0; // the scales of the tiles in flight
   static constexpr size_t kBytes = 1024 + 2 * (size_t)kPxRows * 256 + (size_t)kSlots * kPxTileBytes +
                                    (size_t)kRaw * kPxRawBytes + (size_t)kScaleSlots * kPxTile * 4 +
-                                   (2 * 5 + 2 * 2 + 2 * 3 + 5) * 8 + 16;
+                                   (2 * 5 + 2 * 2 + 2 * 3 + 12) * 8 + 16;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -62,7 +62,7 @@ struct PxSmem {
   using C = PxCfg<KV>;
   uint8_t *q, *ring, *raw;
   float *scale;
-  uint64_t *full, *empty, *raw_full, *raw_empty, *sc_full, *sc_empty, *s_full, *p_full, *done;
+  uint64_t *full, *empty, *raw_full, *raw_empty, *sc_full, *sc_empty, *s_full, *p_full, *o_done, *done;
   uint32_t *tmem_base;
   volatile int *abort_flag;
   __device__ explicit PxSmem(uint8_t *p) {
@@ -77,19 +77,19 @@ struct PxSmem {
     sc_full = raw_empty + 2;
     sc_empty = sc_full + 3;
     s_full = sc_empty + 3;
-    p_full = s_full + 2;
-    done = p_full + 2;
-    tmem_base = reinterpret_cast<uint32_t *>(done + 1);
+    p_full = s_full + 4;
+    o_done = p_full + 4;
+    done = o_done + 2;
+    tmem_base = reinterpret_cast<uint32_t *>(done + 2);
     abort_flag = reinterpret_cast<volatile int *>(tmem_base + 1);
   }
 };
 
-// The pair's rows, and a walk over its tiles: the prefix's, then each sequence's own.
+// The pair's rows, and a walk over the own tiles of its sequences.
 struct PxWalk {
   int64_t row0;               // first row of the pair
   int b_last, i_last;         // sequence and query token of its last row
-  int t;                      // tile of the list
-  int b, j, count;            // own tiles: sequence, tile j of its count
+  int b, j, count;            // sequence, tile j of its count
 
   __device__ __forceinline__ int own_tiles(const PrefixParams &P, int seq) const {
     const int i = seq == b_last ? i_last : P.n_q - 1;
@@ -102,85 +102,68 @@ struct PxWalk {
     b_last = q / P.n_q;
     i_last = q - b_last * P.n_q;
     b = (int)(row0 / P.n_heads) / P.n_q;
-    t = j = 0;
+    j = 0;
     count = own_tiles(P, b);
   }
-  __device__ __forceinline__ int total(const PrefixParams &P) const {
-    int n = P.n_tiles;
+  __device__ __forceinline__ int total(const PrefixParams &P) const {   // own tiles of the pair
+    int n = 0;
     for (int s = b; s <= b_last; ++s) n += own_tiles(P, s);
     return n;
   }
   __device__ __forceinline__ void seek(const PrefixParams &P, int tile) {
-    t = tile;
-    j = tile - P.n_tiles;
+    j = tile;
     while (j >= count && b < b_last) {
       j -= count;
       count = own_tiles(P, ++b);
     }
   }
   __device__ __forceinline__ void next(const PrefixParams &P) {
-    ++t;
-    if (++j >= count && t > P.n_tiles && b < b_last) {
+    if (++j >= count && b < b_last) {
       j = 0;
       count = own_tiles(P, ++b);
     }
   }
-  __device__ __forceinline__ bool own(const PrefixParams &P) const { return t >= P.n_tiles; }
+  __device__ __forceinline__ int64_t y(const PrefixParams &P) const { return P.seq.start[b] + j * kPxTile; }
   // rows of the tile that exist for this pair (may exceed the tile)
   __device__ __forceinline__ int valid(const PrefixParams &P) const {
-    if (!own(P)) return P.prefix_len - t * kPxTile;
     return P.seq.len[b] - P.n_q + (b == b_last ? i_last : P.n_q - 1) + 1 - j * kPxTile;
   }
-  // lanes [lo, hi) of block g that see some row of the tile
-  __device__ __forceinline__ void lanes(const PrefixParams &P, int g, int &lo, int &hi) const {
+  // lanes [lo, hi) of block g that see some row of the tile; `rows`: the block's rows
+  __device__ __forceinline__ void lanes(const PrefixParams &P, int g, int rows, int &lo, int &hi) const {
     const int64_t r0 = row0 + g * kPxRows;
-    hi = (int)min((int64_t)kPxRows, P.rows - r0);
-    lo = 0;
-    if (own(P)) {
-      const int i = max(0, j * kPxTile - (P.seq.len[b] - P.n_q));   // first query token that reaches it
-      lo = (int)max((int64_t)0, ((int64_t)b * P.n_q + i) * P.n_heads - r0);
-      hi = (int)min((int64_t)hi, ((int64_t)b + 1) * P.n_q * P.n_heads - r0);
-    }
+    const int i = max(0, j * kPxTile - (P.seq.len[b] - P.n_q));   // first query token that reaches it
+    lo = (int)max((int64_t)0, ((int64_t)b * P.n_q + i) * P.n_heads - r0);
+    hi = (int)min((int64_t)rows, ((int64_t)b + 1) * P.n_q * P.n_heads - r0);
   }
 };
 
-// bounded wait by lane 0, the result broadcast to the warp (records a timeout)
-__device__ __forceinline__ bool px_wait(const PrefixParams &P, volatile int *abort_flag,
-                                        uint64_t *bar, uint32_t parity) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) {
-    ok = mbar_wait(smem_u32(bar), parity);
-    if (!ok) {
-      record_status(P.status, kStatusTimeout);
-      *abort_flag = 1;
-    }
-    if (*abort_flag) ok = false;
+// P of 32 columns from their scores: exp2(x sc - m) as bf16 pairs, times the V scales (e4m3); the sum
+// (before the V scales) is added to ls. All exponentials on the special-function unit: moving 4, 6 or 8 of 16
+// to the FMA pipe by a quartic took 32 x 1 x 32 heads behind 131,072 from 93 to 96, 101 and 108 us.
+template <bool kFp8>
+__device__ __forceinline__ void px_weights(const float (&x)[32], float2 sc2, float2 neg, const float *vsc, float2 &ls,
+                                           uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 z = ffma2(make_float2(x[2 * k], x[2 * k + 1]), sc2, neg);
+    float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+    ls = fadd2(ls, e);
+    if (kFp8) e = fmul2(e, *reinterpret_cast<const float2 *>(vsc + 2 * k));
+    pk[k] = pack_bf16(e.x, e.y);
   }
-  return __shfl_sync(0xffffffffu, ok, 0);
 }
 
-// 32 scores of this thread's row: columns of S from TMEM, times their K scales (e4m3), -inf from
-// column `valid` on.
-template <bool kFp8>
-__device__ __forceinline__ void px_scores(uint32_t addr, const float *ksc, int valid, float (&x)[32]) {
-  tmem_ld32(addr, x);
-  tmem_wait_ld();
-  if (kFp8) {
+// 32 scores of this thread's row times their K scales (e4m3).
+__device__ __forceinline__ void px_scale(float (&x)[32], const float *ksc) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const float4 f = *reinterpret_cast<const float4 *>(ksc + i);
-      const float2 a = fmul2(make_float2(x[i], x[i + 1]), make_float2(f.x, f.y));
-      const float2 b = fmul2(make_float2(x[i + 2], x[i + 3]), make_float2(f.z, f.w));
-      x[i] = a.x;
-      x[i + 1] = a.y;
-      x[i + 2] = b.x;
-      x[i + 3] = b.y;
-    }
-  }
-  if (valid < 32) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i >= valid) x[i] = -INFINITY;
+  for (int i = 0; i < 32; i += 4) {
+    const float4 f = *reinterpret_cast<const float4 *>(ksc + i);
+    const float2 a = fmul2(make_float2(x[i], x[i + 1]), make_float2(f.x, f.y));
+    const float2 b = fmul2(make_float2(x[i + 2], x[i + 3]), make_float2(f.z, f.w));
+    x[i] = a.x;
+    x[i + 1] = a.y;
+    x[i + 2] = b.x;
+    x[i + 3] = b.y;
   }
 }
 
@@ -194,17 +177,19 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
   // neighbouring CTAs take the same tiles for different rows, so that these are read from HBM once
   const int pair = blockIdx.x % P.n_pairs, split = blockIdx.x / P.n_pairs;
   PxWalk W(P, pair);
-  const int total = W.total(P);
+  const int total = P.n_tiles + W.total(P);
   const int tile0 = (int)((int64_t)split * total / P.n_splits);
   const int n = (int)((int64_t)(split + 1) * total / P.n_splits) - tile0;
   const int64_t row0 = W.row0;
-  const int nb = P.rows - row0 > kPxRows ? 2 : 1;   // blocks with rows
-  W.seek(P, tile0);
+  const int nb = P.rows - row0 > kPxRows ? 2 : 1;     // blocks with rows
+  const int np = max(0, min(n, P.n_tiles - tile0));   // the first np tiles are the prefix's, the others own ones
+  W.seek(P, max(0, tile0 - P.n_tiles));
+  const int rows_g[2] = {(int)min((int64_t)kPxRows, P.rows - row0), (int)min((int64_t)kPxRows, P.rows - row0 - kPxRows)};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(smem_u32(&sm.full[s]), C::kFp8 ? 4 : 1);
-      mbar_init(smem_u32(&sm.empty[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), nb);
     }
     for (int s = 0; s < C::kRaw; ++s) {
       mbar_init(smem_u32(&sm.raw_full[s]), 1);
@@ -214,11 +199,14 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
       mbar_init(smem_u32(&sm.sc_full[s]), 32);
       mbar_init(smem_u32(&sm.sc_empty[s]), 4 * nb);
     }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(smem_u32(&sm.s_full[g]), 1);
-      mbar_init(smem_u32(&sm.p_full[g]), 4);
+    for (int i = 0; i < 4; ++i) {   // block i / 2, half i % 2
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
     }
+    mbar_init(smem_u32(&sm.o_done[0]), 1);
+    mbar_init(smem_u32(&sm.o_done[1]), 1);
     mbar_init(smem_u32(&sm.done[0]), 1);
+    mbar_init(smem_u32(&sm.done[1]), 1);
     *sm.abort_flag = 0;
     fence_barrier_init();
   }
@@ -242,7 +230,10 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
 
   const int g = warp >> 2;                             // softmax warps: the block
   const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-  if (warp < 8) {   // Q blocks -> shared memory (K-major, 128-byte swizzle), zeros behind the last row
+  const int64_t row = row0 + g * kPxRows + (warp & 3) * 32 + lane;   // softmax warps: the thread's row
+  float m_run = -INFINITY, l_run = 0.f;
+  if (warp < 8) {
+    // Q blocks -> shared memory (K-major, 128-byte swizzle), zeros behind the last row
     const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(P.q) + row0 * kHeadDim;
     const int64_t left = P.rows - row0;
 #pragma unroll 8
@@ -261,267 +252,320 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
       tmem_wait_st();
     }
     tc_fence_before();
-    asm volatile("bar.arrive 1, 288;" ::: "memory");   // the MMA warp waits for these alone
-  }
-
-  float m_run = -INFINITY, l_run = 0.f;
-  if (warp == kPxWarpTma) {
-    // ------------------------------------------------------------ producer
-    int it = 0;
-    for (; it < 2 * n; ++it) {   // K_0, V_0, K_1, V_1, ...
-      const bool own = W.own(P), is_v = it & 1;
-      const CUtensorMap *map = own ? (is_v ? &tm.v : &tm.k) : (is_v ? &tm.pv : &tm.pk);
-      const int y = own ? (int)P.seq.start[W.b] + W.j * kPxTile : W.t * kPxTile;
-      if constexpr (!C::kFp8) {
-        const int s = it % C::kSlots;
-        if (it >= C::kSlots && !px_wait(P, sm.abort_flag, &sm.empty[s], ((it / C::kSlots) & 1) ^ 1)) break;
-        if (lane == 0) {
-          const uint32_t st = smem_u32(sm.ring + s * kPxTileBytes), bar = smem_u32(&sm.full[s]);
-          mbar_arrive_expect_tx(bar, kPxTileBytes);
-          tma_load_2d(st, map, bar, 0, y);
-          tma_load_2d(st + kPxTile * 128, map, bar, 64, y);
+    asm volatile("bar.arrive 1, 320;" ::: "memory");   // the MMA warps wait for these alone
+    if (g < nb) {
+      // ------------------------------------------------------------ softmax
+      const uint32_t s_addr = lane_addr + g * 128, o_addr = lane_addr + 256 + g * 128;
+      const float sc = P.scale_log2;
+      const float2 sc2 = make_float2(sc, sc);
+      const int rl = (warp & 3) * 32 + lane;
+      const int my_q = (int)(row / P.n_heads);           // flat query token
+      int c_s = 0;                                       // tiles that concerned this block
+      for (int it = 0; it < n; ++it) {
+        int lo = 0, hi = rows_g[g], tile_valid = P.prefix_len - (tile0 + it) * kPxTile, valid = tile_valid;
+        const bool own = it >= np;
+        if (own) {
+          W.lanes(P, g, rows_g[g], lo, hi);
+          tile_valid = W.valid(P);
+          valid = (rl >= lo && rl < hi) ? P.seq.len[W.b] - P.n_q + (my_q - W.b * P.n_q) + 1 - W.j * kPxTile : 0;
+          W.next(P);
         }
-      } else {
-        const int s = it % C::kRaw, c = it % C::kScaleSlots;
-        if (it >= C::kRaw && !px_wait(P, sm.abort_flag, &sm.raw_empty[s], ((it / C::kRaw) & 1) ^ 1)) break;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&sm.raw_full[s]);
-          mbar_arrive_expect_tx(bar, kPxRawBytes);
-          tma_load_2d(smem_u32(sm.raw + s * kPxRawBytes), map, bar, 0, y);
+        const float *ksc = sm.scale, *vsc = sm.scale;
+        if constexpr (C::kFp8) {
+          const int tk = 2 * it, tv = 2 * it + 1;
+          if (!warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[tk % C::kScaleSlots], (tk / C::kScaleSlots) & 1)) break;
+          if (!warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[tv % C::kScaleSlots], (tv / C::kScaleSlots) & 1)) break;
+          ksc += (tk % C::kScaleSlots) * kPxTile;
+          vsc += (tv % C::kScaleSlots) * kPxTile;
         }
-        if (it >= C::kScaleSlots && !px_wait(P, sm.abort_flag, &sm.sc_empty[c], ((it / C::kScaleSlots) & 1) ^ 1)) break;
-        const float *sc = (is_v ? P.v_scale : P.k_scale) + (own ? 0 : P.prefix_start) + y;
-        const int valid = W.valid(P);
+        if (hi > lo) {
+          const bool mine = lo < (warp & 3) * 32 + 32 && hi > (warp & 3) * 32;   // some lane of this warp
+          bool ok = true;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = u * 32 + lane;
-          const bool in = r < valid;
-          cp_async_4(smem_u32(sm.scale + c * kPxTile + r), sc + (in ? r : 0), in ? 4u : 0u);
-        }
-        cp_async_mbar_arrive(smem_u32(&sm.sc_full[c]));
-      }
-      if (is_v) W.next(P);
-      __syncwarp();
-    }
-    if (it < 2 * n && lane == 0) {   // gave up: the copies in flight land before the CTA ends
-      constexpr int N = C::kFp8 ? C::kRaw : C::kSlots;
-      for (int j = max(0, it - N); j < it; ++j)
-        mbar_wait(smem_u32(C::kFp8 ? &sm.raw_full[j % N] : &sm.full[j % N]), (j / N) & 1);
-    }
-    if constexpr (C::kFp8) asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncwarp();
-  } else if (C::kFp8 && warp >= kPxWarpWiden) {
-    // ------------------------------------------------------------ e4m3 codes -> bf16 tiles
-    // 16 codes per thread and step: eight neighbouring threads take four chunks of two rows, which
-    // the swizzle spreads over all banks
-    const int t = threadIdx.x - kPxWarpWiden * 32;
-    for (int it = 0; it < 2 * n; ++it) {
-      const int r = it % 2, s = it % C::kSlots;
-      if (!px_wait(P, sm.abort_flag, &sm.raw_full[r], (it / 2) & 1)) break;
-      if (it >= C::kSlots && !px_wait(P, sm.abort_flag, &sm.empty[s], ((it / C::kSlots) & 1) ^ 1)) break;
-      const int valid = W.valid(P);
-      const uint8_t *src = sm.raw + r * kPxRawBytes;
-      uint8_t *dst = sm.ring + s * kPxTileBytes;
-#pragma unroll 2
-      for (int u = 0; u < 8; ++u) {
-        const int e = u * 128 + t;                     // (row pair, half, row of the pair, chunk)
-        const int row = (e >> 4) * 2 + ((e >> 2) & 1), ch = ((e >> 3) & 1) * 4 + (e & 3);
-        uint4 c = *reinterpret_cast<const uint4 *>(src + row * 128 + ch * 16);
-        if (row >= valid) c = make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          o[2 * j] = e4m3x2_to_bf16x2((uint16_t)(w[j] & 0xffffu));
-          o[2 * j + 1] = e4m3x2_to_bf16x2((uint16_t)(w[j] >> 16));
-        }
-        uint8_t *box = dst + (ch >> 2) * (kPxTile * 128);
-        *reinterpret_cast<uint4 *>(box + sw128(row, (ch & 3) * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(box + sw128(row, (ch & 3) * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&sm.full[s]));
-        mbar_arrive(smem_u32(&sm.raw_empty[r]));
-      }
-      if (it & 1) W.next(P);
-    }
-  } else if (warp == kPxWarpMma) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t id_s = umma_idesc_bf16(kPxRows, kPxTile);
-    const uint32_t id_o = umma_idesc_bf16_bmn(kPxRows, kHeadDim);
-    const uint32_t qs = smem_u32(sm.q), ring = smem_u32(sm.ring);
-    asm volatile("bar.sync 1, 288;" ::: "memory");     // Q and O are ready
-    tc_fence_after();
-    int lo[2] = {}, hi[2] = {};                        // lanes of each block in tile it - 1
-    int done_s[2] = {0, 0};                            // products S issued
-    for (int it = 0; it <= n; ++it) {
-      const int tk = 2 * it, tv = 2 * it - 1;          // ring positions of K_it and V_(it - 1)
-      if (it < n && !px_wait(P, sm.abort_flag, &sm.full[tk % C::kSlots], (tk / C::kSlots) & 1)) break;
-      if (it >= 1 && !px_wait(P, sm.abort_flag, &sm.full[tv % C::kSlots], (tv / C::kSlots) & 1)) break;
-      const uint32_t ks = ring + (tk % C::kSlots) * kPxTileBytes;
-      const uint32_t vs = ring + (it >= 1 ? tv % C::kSlots : 0) * kPxTileBytes;
-      bool ok = true;
-#pragma unroll
-      for (int g2 = 0; g2 < 2; ++g2) {
-        int nlo = 0, nhi = 0;
-        if (it < n && g2 < nb) W.lanes(P, g2, nlo, nhi);
-        if (it >= 1 && hi[g2] > lo[g2]) {   // O_g += P_g . V_(it - 1) on those lanes
-          if (!px_wait(P, sm.abort_flag, &sm.p_full[g2], (done_s[g2] - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            uint32_t off[4];                 // lanes left as they are
-#pragma unroll
-            for (int w = 0; w < 4; ++w) off[w] = ~lane_bits(lo[g2] - 32 * w, hi[g2] - 32 * w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_bf16_ts_lanes(tmem + 256 + g2 * 128, tmem + g2 * 128 + 8 * k,
-                                 umma_desc_sw128_mn(vs + k * 2048, kPxTile * 128, 1024), id_o, off);
-            if (g2 == 1 || hi[1] <= lo[1]) umma_commit(smem_u32(&sm.empty[tv % C::kSlots]));
-          }
-          __syncwarp();
-        }
-        lo[g2] = nlo;
-        hi[g2] = nhi;
-        if (nhi > nlo) {   // S_g = Q_g . K_it^T, over the P_g that the product before has read
-          tc_fence_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t o = (k >> 2) * (kPxTile * 128) + (k & 3) * 32;
-              umma_bf16(tmem + g2 * 128, umma_desc_sw128(qs + g2 * (kPxRows * 256) + o, 1024),
-                        umma_desc_sw128(ks + o, 1024), id_s, k > 0);
+          for (int h = 0; h < 2 && ok; ++h) {   // columns 64 h .. + 63
+            ok = warp_wait_all(P.status, sm.abort_flag, &sm.s_full[2 * g + h], c_s & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (h == 0 && own && !C::kFp8 && tile_valid < kPxTile) {   // V rows behind the sequence's last: zero
+              const int tv = 2 * it + 1;
+              ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[tv % C::kSlots], (tv / C::kSlots) & 1);
+              if (!ok) break;
+              uint8_t *vt = sm.ring + (tv % C::kSlots) * kPxTileBytes;
+              for (int e = tile_valid * 16 + (threadIdx.x & 127); e < kPxTile * 16; e += 128)
+                *reinterpret_cast<uint4 *>(vt + (e & 1) * (kPxTile * 128) + (e >> 1) * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
             }
-            umma_commit(smem_u32(&sm.s_full[g2]));
-          }
-          __syncwarp();
-          ++done_s[g2];
-        }
-      }
-      if (!ok) break;
-      if (it < n) {
-        if (lane == 0) umma_commit(smem_u32(&sm.empty[tk % C::kSlots]));
-        __syncwarp();
-        W.next(P);
-      }
-    }
-    if (lane == 0) {   // every issued product has landed before TMEM is read or released
-      umma_commit(smem_u32(&sm.done[0]));
-      if (!mbar_wait(smem_u32(&sm.done[0]), 0)) {
-        record_status(P.status, kStatusTimeout);
-        *sm.abort_flag = 1;
-      }
-    }
-    __syncwarp();
-  }
-  const int64_t row = row0 + g * kPxRows + (warp & 3) * 32 + lane;   // softmax warps: the thread's row
-  if (warp < 8 && g < nb) {
-    // ------------------------------------------------------------ softmax
-    const uint32_t s_addr = lane_addr + g * 128, o_addr = lane_addr + 256 + g * 128;
-    const float sc = P.scale_log2;
-    const float2 sc2 = make_float2(sc, sc);
-    const int rl = (warp & 3) * 32 + lane;
-    const int my_q = (int)(row / P.n_heads);           // flat query token
-    int c_s = 0;                                       // tiles that concerned this block
-    for (int it = 0; it < n; ++it) {
-      int lo, hi;
-      W.lanes(P, g, lo, hi);
-      const bool own = W.own(P);
-      const int tile_valid = W.valid(P);
-      int valid = tile_valid;
-      if (own) valid = (rl >= lo && rl < hi) ? P.seq.len[W.b] - P.n_q + (my_q - W.b * P.n_q) + 1 - W.j * kPxTile : 0;
-      W.next(P);
-      const float *ksc = sm.scale, *vsc = sm.scale;
-      if constexpr (C::kFp8) {
-        const int tk = 2 * it, tv = 2 * it + 1;
-        if (!px_wait(P, sm.abort_flag, &sm.sc_full[tk % C::kScaleSlots], (tk / C::kScaleSlots) & 1)) break;
-        if (!px_wait(P, sm.abort_flag, &sm.sc_full[tv % C::kScaleSlots], (tv / C::kScaleSlots) & 1)) break;
-        ksc += (tk % C::kScaleSlots) * kPxTile;
-        vsc += (tv % C::kScaleSlots) * kPxTile;
-      }
-      if (hi > lo) {
-        if (!px_wait(P, sm.abort_flag, &sm.s_full[g], c_s & 1)) break;
-        tc_fence_after();
-        if (own && !C::kFp8 && tile_valid < kPxTile) {   // V rows behind the sequence's last: zero
-          const int tv = 2 * it + 1;
-          if (!px_wait(P, sm.abort_flag, &sm.full[tv % C::kSlots], (tv / C::kSlots) & 1)) break;
-          uint8_t *vt = sm.ring + (tv % C::kSlots) * kPxTileBytes;
-          for (int e = tile_valid * 16 + (threadIdx.x & 127); e < kPxTile * 16; e += 128)
-            *reinterpret_cast<uint4 *>(vt + (e & 1) * (kPxTile * 128) + (e >> 1) * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        if (lo < (warp & 3) * 32 + 32 && hi > (warp & 3) * 32) {   // some lane of this warp
-          // the row maximum; the scores stay in TMEM and are read again below
-          float mt = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            float x[32];
-            px_scores<C::kFp8>(s_addr + c, ksc + c, valid - c, x);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) mt = fmax3(mt, x[i], x[i + 1]);
-          }
-          mt *= sc;
-          const bool move = mt > m_run + kPxLazy;
-          if (__any_sync(0xffffffffu, move)) {
-            const float m_new = move ? mt : m_run;
-            const float alpha = move ? (m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new)) : 1.f;
-            l_run *= alpha;
-            m_run = m_new;
-            if (c_s > 0) {   // rescale this row of O (S has landed, and so the products before it)
-#pragma unroll 1
-              for (int c = 0; c < 128; c += 32) {
-                float v[32];
-                tmem_ld32(o_addr + c, v);
-                tmem_wait_ld();
-                uint32_t u[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * alpha);
-                tmem_st32(o_addr + c, u);
+            if (mine) {
+              float x[2][32];
+              tmem_ld32_issue(s_addr + h * 64, x[0]);
+              tmem_ld32_issue(s_addr + h * 64 + 32, x[1]);
+              tmem_wait_ld32(x[0]);
+              tmem_wait_ld32(x[1]);
+              if constexpr (C::kFp8) {
+                px_scale(x[0], ksc + h * 64);
+                px_scale(x[1], ksc + h * 64 + 32);
               }
+              if (__any_sync(0xffffffffu, valid < h * 64 + 64)) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                  if (h * 64 + i >= valid) x[i >> 5][i & 31] = -INFINITY;
+              }
+              float mq[4];   // the row maximum
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float *xc = x[c >> 1] + (c & 1) * 16;
+                mq[c] = fmaxf(xc[0], xc[1]);
+#pragma unroll
+                for (int i = 2; i < 16; i += 2) mq[c] = fmax3(mq[c], xc[i], xc[i + 1]);
+              }
+              const float mt = fmaxf(fmax3(mq[0], mq[1], mq[2]), mq[3]) * sc;
+              const bool move = mt > m_run + kPxLazy;
+              if (__any_sync(0xffffffffu, move)) {
+                const float m_new = move ? mt : m_run;
+                const float alpha = move ? (m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new)) : 1.f;
+                l_run *= alpha;
+                m_run = m_new;
+                if (c_s > 0 || h > 0) {   // rescale this row of O once the last product, number 2 c_s + h - 1, is
+                                          // done (those before it are: this S was issued behind them)
+                  ok = warp_wait_all(P.status, sm.abort_flag, &sm.o_done[g], (h ^ 1) & 1);
+                  if (!ok) break;
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int c = 0; c < 128; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_issue(o_addr + c, v);
+                    tmem_wait_ld16(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                    tmem_st16(o_addr + c, v);
+                  }
+                  tmem_wait_st();
+                }
+              }
+              const float mref = (m_run == -INFINITY) ? 0.f : m_run;
+              const float2 neg = make_float2(-mref, -mref);
+              float2 ls = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
+                px_weights<C::kFp8>(x[c], sc2, neg, vsc + h * 64 + c * 32, ls, pk);
+                tmem_st16(s_addr + h * 64 + c * 16, pk);   // over scores that are in registers
+              }
+              l_run += ls.x + ls.y;
               tmem_wait_st();
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[2 * g + h]));
           }
-          const float mref = (m_run == -INFINITY) ? 0.f : m_run;
-          const float2 neg = make_float2(-mref, -mref);
-          float2 ls = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            float x[32];
-            px_scores<C::kFp8>(s_addr + c, ksc + c, valid - c, x);
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 z = ffma2(make_float2(x[2 * k], x[2 * k + 1]), sc2, neg);
-              float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-              ls = fadd2(ls, e);
-              if (C::kFp8) e = fmul2(e, *reinterpret_cast<const float2 *>(vsc + c + 2 * k));
-              pk[k] = pack_bf16(e.x, e.y);
-            }
-            tmem_st16(s_addr + c / 2, pk);   // columns that have been read
-          }
-          l_run += ls.x + ls.y;
-          tmem_wait_st();
+          if (!ok) break;
+          ++c_s;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[g]));
-        ++c_s;
+        if constexpr (C::kFp8) {
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sm.sc_empty[(2 * it) % C::kScaleSlots]));
+            mbar_arrive(smem_u32(&sm.sc_empty[(2 * it + 1) % C::kScaleSlots]));
+          }
+        }
       }
-      if constexpr (C::kFp8) {
+    }
+  } else {
+    if (warp == kPxWarpTma) {
+      // ------------------------------------------------------------ producer
+      int it = 0;
+      for (; it < 2 * n; ++it) {   // K_0, V_0, K_1, V_1, ...
+        const bool own = (it >> 1) >= np, is_v = it & 1;
+        const CUtensorMap *map = own ? (is_v ? &tm.v : &tm.k) : (is_v ? &tm.pv : &tm.pk);
+        const int y = own ? (int)W.y(P) : (tile0 + (it >> 1)) * kPxTile;
+        if constexpr (!C::kFp8) {
+          const int s = it % C::kSlots;
+          if (it >= C::kSlots && !warp_wait_all(P.status, sm.abort_flag, &sm.empty[s], ((it / C::kSlots) & 1) ^ 1)) break;
+          if (lane == 0) {
+            const uint32_t st = smem_u32(sm.ring + s * kPxTileBytes), bar = smem_u32(&sm.full[s]);
+            mbar_arrive_expect_tx(bar, kPxTileBytes);
+            tma_load_2d(st, map, bar, 0, y);
+            tma_load_2d(st + kPxTile * 128, map, bar, 64, y);
+          }
+        } else {
+          const int s = it % C::kRaw, c = it % C::kScaleSlots;
+          if (it >= C::kRaw && !warp_wait_all(P.status, sm.abort_flag, &sm.raw_empty[s], ((it / C::kRaw) & 1) ^ 1)) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&sm.raw_full[s]);
+            mbar_arrive_expect_tx(bar, kPxRawBytes);
+            tma_load_2d(smem_u32(sm.raw + s * kPxRawBytes), map, bar, 0, y);
+          }
+          if (it >= C::kScaleSlots && !warp_wait_all(P.status, sm.abort_flag, &sm.sc_empty[c], ((it / C::kScaleSlots) & 1) ^ 1)) break;
+          const float *sc = (is_v ? P.v_scale : P.k_scale) + (own ? 0 : P.prefix_start) + y;
+          const int valid = own ? W.valid(P) : P.prefix_len - y;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = u * 32 + lane;
+            const bool in = r < valid;
+            cp_async_4(smem_u32(sm.scale + c * kPxTile + r), sc + (in ? r : 0), in ? 4u : 0u);
+          }
+          cp_async_mbar_arrive(smem_u32(&sm.sc_full[c]));
+        }
+        if (is_v && own) W.next(P);
+        __syncwarp();
+      }
+      if (it < 2 * n && lane == 0) {   // gave up: the copies in flight land before the CTA ends
+        constexpr int N = C::kFp8 ? C::kRaw : C::kSlots;
+        for (int j = max(0, it - N); j < it; ++j)
+          mbar_wait(smem_u32(C::kFp8 ? &sm.raw_full[j % N] : &sm.full[j % N]), (j / N) & 1);
+      }
+      if constexpr (C::kFp8) asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+    } else if (C::kFp8 && warp >= kPxWarpWiden) {
+      // ------------------------------------------------------------ e4m3 codes -> bf16 tiles
+      // 16 codes per thread and step: eight neighbouring threads take four chunks of two rows, which
+      // the swizzle spreads over all banks
+      const int t = threadIdx.x - kPxWarpWiden * 32;
+      for (int it = 0; it < 2 * n; ++it) {
+        const int r = it % 2, s = it % C::kSlots;
+        if (!warp_wait_all(P.status, sm.abort_flag, &sm.raw_full[r], (it / 2) & 1)) break;
+        if (it >= C::kSlots && !warp_wait_all(P.status, sm.abort_flag, &sm.empty[s], ((it / C::kSlots) & 1) ^ 1)) break;
+        const bool own = (it >> 1) >= np;
+        const int valid = own ? W.valid(P) : kPxTile;   // (the prefix's maps end with it)
+        const uint8_t *src = sm.raw + r * kPxRawBytes;
+        uint8_t *dst = sm.ring + s * kPxTileBytes;
+#pragma unroll 2
+        for (int u = 0; u < 8; ++u) {
+          const int e = u * 128 + t;                     // (row pair, half, row of the pair, chunk)
+          const int row = (e >> 4) * 2 + ((e >> 2) & 1), ch = ((e >> 3) & 1) * 4 + (e & 3);
+          uint4 c = *reinterpret_cast<const uint4 *>(src + row * 128 + ch * 16);
+          if (row >= valid) c = make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[2 * j] = e4m3x2_to_bf16x2((uint16_t)(w[j] & 0xffffu));
+            o[2 * j + 1] = e4m3x2_to_bf16x2((uint16_t)(w[j] >> 16));
+          }
+          uint8_t *box = dst + (ch >> 2) * (kPxTile * 128);
+          *reinterpret_cast<uint4 *>(box + sw128(row, (ch & 3) * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(box + sw128(row, (ch & 3) * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&sm.sc_empty[(2 * it) % C::kScaleSlots]));
-          mbar_arrive(smem_u32(&sm.sc_empty[(2 * it + 1) % C::kScaleSlots]));
+          mbar_arrive(smem_u32(&sm.full[s]));
+          mbar_arrive(smem_u32(&sm.raw_empty[r]));
+        }
+        if ((it & 1) && own) W.next(P);
+      }
+    } else if (warp == kPxWarpMma || warp == kPxWarpMma + 1) {
+      // ------------------------------------------------------------ MMA issuers, one warp per block
+      // S runs a tile ahead of P . V: while the softmax warps work on one 64-column buffer the other is
+      // filled, and each P . V is followed by the S that takes its buffer.
+      const int g2 = warp - kPxWarpMma;
+      asm volatile("bar.sync 1, 320;" ::: "memory");   // Q and O are ready
+      tc_fence_after();
+      const uint32_t id_s = umma_idesc_bf16(kPxRows, 64);
+      const uint32_t id_o = umma_idesc_bf16_bmn(kPxRows, kHeadDim);
+      // operand descriptors: the address field counts 16 bytes
+      const uint64_t q_desc = umma_desc_sw128(smem_u32(sm.q) + g2 * (kPxRows * 256), 1024);
+      const uint64_t k_desc = umma_desc_sw128(smem_u32(sm.ring), 1024);
+      const uint64_t v_desc = umma_desc_sw128_mn(smem_u32(sm.ring), kPxTile * 128, 1024);
+      const uint32_t s_tmem = tmem + g2 * 128, o_tmem = tmem + 256 + g2 * 128;
+      const bool issuer = elect_one();                 // the operands stay warp-uniform
+      const int rows = g2 == 0 ? rows_g[0] : rows_g[1];
+      bool ok = g2 < nb;
+      int cur = -1, lo = 0, hi = 0;                    // tile of P . V and its lanes; none yet
+      int next = 0, nlo = 0, nhi = 0;                  // tile of S, if it concerns this block, and its lanes
+      int used = 0;                                    // tiles that concerned this block
+      const auto look = [&] {
+        if (next < np) {
+          nlo = 0;
+          nhi = rows;
+        } else if (next < n) {
+          W.lanes(P, g2, rows, nlo, nhi);
+          W.next(P);
+        }
+      };
+      look();
+      while (ok) {
+        // Tiles that do not concern this block go back as they are -- behind the P . V before them, whose
+        // slot the ring needs to bring them.
+        while (cur < 0 && next < n && nhi <= nlo && ok) {
+          for (int t = 2 * next; t < 2 * next + 2 && ok; ++t) {
+            ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[t % C::kSlots], (t / C::kSlots) & 1);
+            if (ok && lane == 0) mbar_arrive(smem_u32(&sm.empty[t % C::kSlots]));
+          }
+          ++next;
+          look();
+        }
+        const bool more = next < n && nhi > nlo;
+        if (!ok || (!more && cur < 0)) break;
+        const int sk = (2 * next) % C::kSlots, tv = 2 * cur + 1, sv = tv % C::kSlots;
+        const uint64_t kd = k_desc + (uint32_t)(sk * (kPxTileBytes >> 4));
+        const uint64_t vd = v_desc + (uint32_t)(sv * (kPxTileBytes >> 4));
+        if (more) ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[sk], ((2 * next) / C::kSlots) & 1);
+        if (ok && cur >= 0) ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[sv], (tv / C::kSlots) & 1);
+        if (!ok) break;
+        const bool every = lo == 0 && hi == kPxRows;
+        uint32_t off[4];       // lanes left as they are
+#pragma unroll
+        for (int w = 0; w < 4; ++w) off[w] = ~lane_bits(lo - 32 * w, hi - 32 * w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (cur >= 0) {      // O += P . V on the tile's lanes
+            ok = warp_wait_all(P.status, sm.abort_flag, &sm.p_full[2 * g2 + h], (used - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (issuer) {
+              if (every) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  umma_bf16_ts(o_tmem, s_tmem + h * 64 + 8 * k, vd + (4 * h + k) * (2048 >> 4), id_o, true);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  umma_bf16_ts_lanes(o_tmem, s_tmem + h * 64 + 8 * k, vd + (4 * h + k) * (2048 >> 4), id_o, off);
+              }
+              umma_commit(smem_u32(&sm.o_done[g2]));
+            }
+            __syncwarp();
+          }
+          if (issuer) {        // S = Q . K^T for 64 rows of K, over the P that the product before has read
+            if (more) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t o = ((k >> 2) * (kPxTile * 128) + (k & 3) * 32) >> 4;
+                umma_bf16(s_tmem + h * 64, q_desc + o, kd + o + h * (64 * 128 >> 4), id_s, k > 0);
+              }
+              umma_commit(smem_u32(&sm.s_full[2 * g2 + h]));
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (issuer) {          // the slots are free once these products are done
+          if (cur >= 0) umma_commit(smem_u32(&sm.empty[sv]));
+          if (more) umma_commit(smem_u32(&sm.empty[sk]));
+        }
+        __syncwarp();
+        cur = -1;
+        if (more) {
+          cur = next++;
+          lo = nlo;
+          hi = nhi;
+          ++used;
+          look();
         }
       }
+      if (issuer && g2 < nb) {   // every issued product has landed before TMEM is read or released
+        umma_commit(smem_u32(&sm.done[g2]));
+        if (!mbar_wait(smem_u32(&sm.done[g2]), 0)) {
+          record_status(P.status, kStatusTimeout);
+          *sm.abort_flag = 1;
+        }
+      }
+      __syncwarp();
     }
   }
   tc_fence_before();
-  __syncthreads();   // the MMA warp has seen every product land
+  __syncthreads();   // the MMA warps have seen every product land
   tc_fence_after();
   const bool aborted = *sm.abort_flag != 0;
   if (warp < 8 && g < nb && !aborted) {

@@ -95,33 +95,6 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Bounded wait by every calling thread: a warp's lanes test the barrier in one instruction, and the
-// callers make the answer warp-uniform by a vote (one lane testing for its warp and a shuffle took
-// the 8192 x 4096 x 4096 product from 138 to 156 us, no vote to 149 us). The usual case, a phase that is complete already, costs one test; a wait that runs out records the
-// timeout, and one of a CTA that gave up elsewhere ends early.
-__device__ __forceinline__ bool gp_wait_slow(uint32_t *status, volatile int *abort_flag, uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 1024; ++i)
-      if (mbar_test_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer() - t0 > kWaitLimitNs) {
-      record_status(status, kStatusTimeout);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ bool gp_wait(uint32_t *status, volatile int *abort_flag, uint64_t *bar, uint32_t parity) {
-  const uint32_t b = smem_u32(bar);
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_test_wait(b, parity)) return true;
-  return gp_wait_slow(status, abort_flag, b, parity);
-}
-
 // One warp's 32 rows x 128 bytes through its square of shared memory: lane = row writes its 8
 // pieces of 16 bytes (swizzled), then each row leaves by 8 neighbouring lanes. `cols`: elements of
 // the row that exist.
@@ -208,8 +181,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
       const int nt = tile % P.n_tiles, mt = tile / P.n_tiles;
       for (int b = 0; b < kb; ++b, ++it) {
         const int s = it % kGpStages;
-        ok = it < kGpStages || gp_wait(P.status, sm.abort_flag, &sm.empty[s], ((it / kGpStages) & 1) ^ 1);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = it < kGpStages || warp_wait_all(P.status, sm.abort_flag, &sm.empty[s], ((it / kGpStages) & 1) ^ 1);
         if (!ok) break;
         if (issuer) {
           if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sm.full[s]), 2 * kGpStageBytes);
@@ -235,8 +207,8 @@ __global__ void __launch_bounds__(kGpThreads, 1)
     for (int tile = first; tile < n_tiles && ok; tile += stride) {
       for (int b = 0; b < kb; ++b, ++it) {
         const int s = it % kGpStages, a = it & 1;
-        ok = gp_wait(P.status, sm.abort_flag, &sm.full[s], (it / kGpStages) & 1) &&
-             (it < 2 || gp_wait(P.status, sm.abort_flag, &sm.acc_empty[a], ((it >> 1) & 1) ^ 1));
+        ok = lanes_wait(P.status, sm.abort_flag, &sm.full[s], (it / kGpStages) & 1) &&
+             (it < 2 || lanes_wait(P.status, sm.abort_flag, &sm.acc_empty[a], ((it >> 1) & 1) ^ 1));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -299,7 +271,7 @@ __global__ void __launch_bounds__(kGpThreads, 1)
         for (int i = 0; i < 4; ++i) {
           if (b0 + i < kb && ok) {
             const int a = it & 1;
-            ok = __all_sync(0xffffffffu, gp_wait(P.status, sm.abort_flag, &sm.acc_full[a], (it >> 1) & 1));
+            ok = warp_wait_all(P.status, sm.abort_flag, &sm.acc_full[a], (it >> 1) & 1);
             tc_fence_after();
             const float s0 = fa[i] * fw[i];
             const float2 sc = make_float2(s0, s0);
