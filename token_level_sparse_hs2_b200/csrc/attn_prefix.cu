@@ -167,6 +167,12 @@ __device__ __forceinline__ void px_scale(float (&x)[32], const float *ksc) {
   }
 }
 
+// Turns of two warps: wait for the partner's pass; pass on (but after the last turn of all).
+__device__ __forceinline__ void px_turn(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void px_pass(int id, int g, bool last) {
+  if (!(g == 1 && last)) asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+}
+
 template <int KV>
 __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixMaps tm, const __grid_constant__ PrefixParams P) {
@@ -261,6 +267,13 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
       const int rl = (warp & 3) * 32 + lane;
       const int my_q = (int)(row / P.n_heads);           // flat query token
       int c_s = 0;                                       // tiles that concerned this block
+      bool ok = true;
+      // The two warps of a scheduler (w and w + 4) take turns at their exponentials while both have prefix
+      // tiles: one's loads, maximum and waits run beside the other's exponentials. (In step, both waited
+      // for the special-function unit and then left it idle.) A warp that gave up keeps taking its turns.
+      const bool both = nb == 2;
+      const int my_turn = 2 + (warp & 3) * 2 + g, your_turn = my_turn ^ 1;
+      if (both && np > 0 && g == 1) px_pass(your_turn, 0, false);
       for (int it = 0; it < n; ++it) {
         int lo = 0, hi = rows_g[g], tile_valid = P.prefix_len - (tile0 + it) * kPxTile, valid = tile_valid;
         const bool own = it >= np;
@@ -273,29 +286,27 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
         const float *ksc = sm.scale, *vsc = sm.scale;
         if constexpr (C::kFp8) {
           const int tk = 2 * it, tv = 2 * it + 1;
-          if (!warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[tk % C::kScaleSlots], (tk / C::kScaleSlots) & 1)) break;
-          if (!warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[tv % C::kScaleSlots], (tv / C::kScaleSlots) & 1)) break;
+          ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[tk % C::kScaleSlots], (tk / C::kScaleSlots) & 1);
+          ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[tv % C::kScaleSlots], (tv / C::kScaleSlots) & 1);
           ksc += (tk % C::kScaleSlots) * kPxTile;
           vsc += (tv % C::kScaleSlots) * kPxTile;
         }
         if (hi > lo) {
           const bool mine = lo < (warp & 3) * 32 + 32 && hi > (warp & 3) * 32;   // some lane of this warp
-          bool ok = true;
+          const bool turns = both && !own;
 #pragma unroll
-          for (int h = 0; h < 2 && ok; ++h) {   // columns 64 h .. + 63
-            ok = warp_wait_all(P.status, sm.abort_flag, &sm.s_full[2 * g + h], c_s & 1);
-            if (!ok) break;
+          for (int h = 0; h < 2; ++h) {   // columns 64 h .. + 63
+            ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.s_full[2 * g + h], c_s & 1);
             tc_fence_after();
-            if (h == 0 && own && !C::kFp8 && tile_valid < kPxTile) {   // V rows behind the sequence's last: zero
+            if (h == 0 && own && !C::kFp8 && tile_valid < kPxTile && ok) {   // V rows behind the sequence's last: zero
               const int tv = 2 * it + 1;
               ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[tv % C::kSlots], (tv / C::kSlots) & 1);
-              if (!ok) break;
               uint8_t *vt = sm.ring + (tv % C::kSlots) * kPxTileBytes;
               for (int e = tile_valid * 16 + (threadIdx.x & 127); e < kPxTile * 16; e += 128)
                 *reinterpret_cast<uint4 *>(vt + (e & 1) * (kPxTile * 128) + (e >> 1) * 16) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
             }
-            if (mine) {
+            if (mine && ok) {
               float x[2][32];
               tmem_ld32_issue(s_addr + h * 64, x[0]);
               tmem_ld32_issue(s_addr + h * 64 + 32, x[1]);
@@ -328,7 +339,6 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
                 if (c_s > 0 || h > 0) {   // rescale this row of O once the last product, number 2 c_s + h - 1, is
                                           // done (those before it are: this S was issued behind them)
                   ok = warp_wait_all(P.status, sm.abort_flag, &sm.o_done[g], (h ^ 1) & 1);
-                  if (!ok) break;
                   tc_fence_after();
 #pragma unroll 1
                   for (int c = 0; c < 128; c += 16) {
@@ -343,27 +353,36 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
                 }
               }
               const float mref = (m_run == -INFINITY) ? 0.f : m_run;
-              const float2 neg = make_float2(-mref, -mref);
+              float2 neg = make_float2(-mref, -mref);
               float2 ls = make_float2(0.f, 0.f);
+              if (turns) {
+                px_turn(my_turn);
+                asm volatile("" : "+f"(neg.x), "+f"(neg.y));   // the exponentials stay behind it
+              }
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 uint32_t pk[16];
                 px_weights<C::kFp8>(x[c], sc2, neg, vsc + h * 64 + c * 32, ls, pk);
                 tmem_st16(s_addr + h * 64 + c * 16, pk);   // over scores that are in registers
               }
+              if (turns) px_pass(your_turn, g, it == np - 1 && h == 1);
               l_run += ls.x + ls.y;
               tmem_wait_st();
+            } else if (turns) {
+              px_turn(my_turn);
+              px_pass(your_turn, g, it == np - 1 && h == 1);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[2 * g + h]));
+            if (lane == 0 && ok) mbar_arrive(smem_u32(&sm.p_full[2 * g + h]));
           }
-          if (!ok) break;
+          if (!ok && !turns) break;
           ++c_s;
         }
+        if (!ok && own) break;
         if constexpr (C::kFp8) {
           __syncwarp();
-          if (lane == 0) {
+          if (lane == 0 && ok) {
             mbar_arrive(smem_u32(&sm.sc_empty[(2 * it) % C::kScaleSlots]));
             mbar_arrive(smem_u32(&sm.sc_empty[(2 * it + 1) % C::kScaleSlots]));
           }
