@@ -179,6 +179,22 @@ def test_one_sequences_nan_stays_its_own(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_query_rows_of_any_magnitude(fp8):
+    c = Case([40, 50], 1, 32, 700, fp8, seed=13)
+    c.q *= torch.exp2(torch.linspace(-100, 5, 32)).bfloat16()[:, None]     # heads from 2^-100 to 2^5
+    c.q[1, 0, 3] = 0
+    c.q[1, 0, 4, 1:] = 0                                                   # one element alone
+    c.check(*c.run())
+    want, lse = c.run()
+    c.q[0, 0, 7, 5], c.q[0, 0, 8, 9] = float("inf"), float("nan")
+    out, lse2 = c.run()
+    keep = torch.ones(32, dtype=torch.bool)
+    keep[7:9] = False
+    assert torch.equal(out[0, 0][keep], want[0, 0][keep]) and torch.equal(out[1], want[1]) and torch.equal(lse2[1], lse[1])
+    assert torch.isnan(out[0, 0, 7:9]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_streams_graphs_repeats(fp8):
     a, b = Case([30] * 9, 1, 32, 6000, fp8, seed=8), Case([200] * 3, 40, 32, 1500, fp8, seed=9)
     want = [c.run() for c in (a, b)]

@@ -19,8 +19,11 @@
 // bf16 (the tensor cores take no wider operand next to bf16 V; half a step, 2^-8 of each weight,
 // averaged over the keys); m, the sums and O are float32.
 //
-// An e4m3 cache (value = scale[t] code): four more warps widen the code tiles to bf16 (exact);
-// the K scale multiplies S's column, the V scale the weight before its rounding.
+// An e4m3 cache (value = scale[t] code): S comes from the cached codes as they are (kind::f8f6f4), the
+// query split into two e4m3 terms after a power of two per row that puts its largest element in
+// [128, 256): hi is q rounded to e4m3, lo the remainder, exact for every element of at least 2^-10 of
+// the row's largest. Four more warps widen the V codes to bf16 (exact). The K scale and the row's power
+// of two multiply S, the V scale the weight before its rounding.
 //
 // Rows of a tile behind the prefix's or the sequence's last never count, whatever the cache
 // holds there: their columns are masked, and their V rows are zero (the prefix's tensor maps end at its
@@ -40,43 +43,61 @@ constexpr int kPxTile = 128;                       // prefix rows per tile
 constexpr int kPxRows = 128;                       // (query, head) rows per block
 constexpr int kPxTileBytes = kPxTile * 256;        // two [128][128 B] swizzled dim blocks
 constexpr int kPxRawBytes = kPxTile * 128;         // a tile of codes
+constexpr int kPxScaleSlots = 4;                   // e4m3: tiles whose scales are in flight
 constexpr float kPxLazy = 8.f;
-constexpr int kPxWarpMma = 8, kPxWarpTma = 10, kPxWarpWiden = 12;   // MMA: a warp per block; 11: nothing
+constexpr int kPxWarpMma = 8, kPxWarpTma = 10, kPxWarpScale = 11, kPxWarpWiden = 12;   // MMA: a warp per block
 constexpr uint32_t kPxCols = 512;                  // S/P at 0 and 128, O at 256 and 384
 
 template <int KV>
 struct PxCfg {
   static constexpr bool kFp8 = KV == kKvFp8;
   static constexpr int kThreads = (kFp8 ? 16 : 12) * 32;
-  static constexpr int kSlots = kFp8 ? 4 : 5;      // ring of bf16 tiles: K_0, V_0, K_1, V_1, ...
-  static constexpr int kRaw = kFp8 ? 2 : 0;        // ring of code tiles
-  static constexpr int kScaleSlots = kFp8 ? 3 : 0; // the scales of the tiles in flight
-  static constexpr size_t kBytes = 1024 + 2 * (size_t)kPxRows * 256 + (size_t)kSlots * kPxTileBytes +
-                                   (size_t)kRaw * kPxRawBytes + (size_t)kScaleSlots * kPxTile * 4 +
-                                   (2 * 5 + 2 * 2 + 2 * 3 + 12) * 8 + 16;
+  // bf16: one ring of five tiles, K_0, V_0, K_1, V_1, ...; e4m3: three tiles of K codes, two of V codes and
+  // two of widened V, and four tiles' scales
+  static constexpr int kKSlots = kFp8 ? 3 : 5, kVSlots = kFp8 ? 2 : 5;
+  static constexpr int kKBytes = kFp8 ? kPxRawBytes : kPxTileBytes;
+  static constexpr int kRaw = kFp8 ? 2 : 0, kScaleSlots = kFp8 ? kPxScaleSlots : 1;
+  static constexpr size_t kKOff = 2 * (size_t)kPxRows * 256;   // behind Q
+  static constexpr size_t kVOff = kFp8 ? kKOff + (size_t)kKSlots * kPxRawBytes : kKOff;
+  static constexpr size_t kRawOff = kVOff + (size_t)kVSlots * kPxTileBytes;
+  static constexpr size_t kScaleOff = kRawOff + (size_t)kRaw * kPxRawBytes;
+  static constexpr size_t kQScaleOff = kScaleOff + (kFp8 ? (size_t)kScaleSlots * 2 * kPxTile * 4 : 0);
+  static constexpr size_t kBarOff = kQScaleOff + (kFp8 ? 2 * kPxRows * 4 : 0);
+  static constexpr int kBars = 2 * 5 + 2 * 2 + 2 * 2 + 2 * 4 + 4 + 4 + 2 + 2;
+  static constexpr size_t kBytes = 1024 + kBarOff + kBars * 8 + 16;
   static_assert(kBytes <= 227 * 1024, "shared memory");
+  // slot and parity of tile it's K and V
+  __device__ static __forceinline__ int ks(int it) { return kFp8 ? it % kKSlots : (2 * it) % kKSlots; }
+  __device__ static __forceinline__ uint32_t kp(int it) { return (kFp8 ? it / kKSlots : (2 * it) / kKSlots) & 1; }
+  __device__ static __forceinline__ int vs(int it) { return kFp8 ? it % kVSlots : (2 * it + 1) % kVSlots; }
+  __device__ static __forceinline__ uint32_t vp(int it) { return (kFp8 ? it / kVSlots : (2 * it + 1) / kVSlots) & 1; }
 };
 
 template <int KV>
 struct PxSmem {
   using C = PxCfg<KV>;
-  uint8_t *q, *ring, *raw;
-  float *scale;
-  uint64_t *full, *empty, *raw_full, *raw_empty, *sc_full, *sc_empty, *s_full, *p_full, *o_done, *done;
+  uint8_t *q, *k, *v, *raw;
+  float *scale, *qscale;      // [slot][K, V][128]; [row]: c log2 e and the row's power of two
+  uint64_t *k_full, *k_empty, *v_full, *v_empty;   // bf16: the same ring
+  uint64_t *raw_full, *raw_empty, *sc_full, *sc_empty, *s_full, *p_full, *o_done, *done;
   uint32_t *tmem_base;
   volatile int *abort_flag;
   __device__ explicit PxSmem(uint8_t *p) {
     q = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
-    ring = q + 2 * kPxRows * 256;
-    raw = ring + C::kSlots * kPxTileBytes;
-    scale = reinterpret_cast<float *>(raw + C::kRaw * kPxRawBytes);
-    full = reinterpret_cast<uint64_t *>(scale + C::kScaleSlots * kPxTile);
-    empty = full + 5;
-    raw_full = empty + 5;
+    k = q + C::kKOff;
+    v = q + C::kVOff;
+    raw = q + C::kRawOff;
+    scale = reinterpret_cast<float *>(q + C::kScaleOff);
+    qscale = reinterpret_cast<float *>(q + C::kQScaleOff);
+    k_full = reinterpret_cast<uint64_t *>(q + C::kBarOff);
+    k_empty = k_full + 5;
+    v_full = C::kFp8 ? k_empty + 5 : k_full;
+    v_empty = C::kFp8 ? v_full + 2 : k_empty;
+    raw_full = k_empty + 5 + 4;
     raw_empty = raw_full + 2;
     sc_full = raw_empty + 2;
-    sc_empty = sc_full + 3;
-    s_full = sc_empty + 3;
+    sc_empty = sc_full + 4;
+    s_full = sc_empty + 4;
     p_full = s_full + 4;
     o_done = p_full + 4;
     done = o_done + 2;
@@ -153,6 +174,44 @@ __device__ __forceinline__ void px_weights(const float (&x)[32], float2 sc2, flo
   }
 }
 
+// Eight elements of a query row as e4m3 terms hi and lo (two [128 rows][128 B] operands), by 16 threads
+// per row; the row's factor c log2 e 2^ex goes to *factor.
+__device__ __forceinline__ void px_split_q(uint4 v, uint8_t *qb, int r, int ch, float scale_log2, float *factor) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float f[8], amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    amax = fmax3(amax, fabsf(f[2 * i]), fabsf(f[2 * i + 1]));
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  // exponents kept in the range whose powers of two are normal both ways
+  const int ex = amax > 0.f ? min(max(ilogbf(amax) - 7, -120), 120) : 0;
+  const float down = __int_as_float((127 - ex) << 23);
+  uint32_t hi[2], lo[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 x = make_float2(f[4 * i + 2 * j] * down, f[4 * i + 2 * j + 1] * down);
+      const __nv_fp8x2_storage_t hc = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hc, __NV_E4M3);
+      const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+      h[j] = hc;
+      l[j] = __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+    }
+    hi[i] = h[0] | (h[1] << 16);
+    lo[i] = l[0] | (l[1] << 16);
+  }
+  *reinterpret_cast<uint2 *>(qb + sw128(r, ch * 8)) = make_uint2(hi[0], hi[1]);
+  *reinterpret_cast<uint2 *>(qb + kPxRows * 128 + sw128(r, ch * 8)) = make_uint2(lo[0], lo[1]);
+  // an infinite element has no such terms: every score of its row is infinite or NaN, and so its softmax NaN
+  if (ch == 0) *factor = amax == INFINITY ? __int_as_float(0x7fc00000) : scale_log2 * __int_as_float((127 + ex) << 23);
+}
+
 // 32 scores of this thread's row times their K scales (e4m3).
 __device__ __forceinline__ void px_scale(float (&x)[32], const float *ksc) {
 #pragma unroll
@@ -193,17 +252,21 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
   const int rows_g[2] = {(int)min((int64_t)kPxRows, P.rows - row0), (int)min((int64_t)kPxRows, P.rows - row0 - kPxRows)};
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(smem_u32(&sm.full[s]), C::kFp8 ? 4 : 1);
-      mbar_init(smem_u32(&sm.empty[s]), nb);
+    for (int s = 0; s < C::kKSlots; ++s) {
+      mbar_init(smem_u32(&sm.k_full[s]), 1);
+      mbar_init(smem_u32(&sm.k_empty[s]), nb);
     }
-    for (int s = 0; s < C::kRaw; ++s) {
-      mbar_init(smem_u32(&sm.raw_full[s]), 1);
-      mbar_init(smem_u32(&sm.raw_empty[s]), 4);
-    }
-    for (int s = 0; s < C::kScaleSlots; ++s) {
-      mbar_init(smem_u32(&sm.sc_full[s]), 32);
-      mbar_init(smem_u32(&sm.sc_empty[s]), 4 * nb);
+    if constexpr (C::kFp8) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(smem_u32(&sm.v_full[s]), 4);
+        mbar_init(smem_u32(&sm.v_empty[s]), nb);
+        mbar_init(smem_u32(&sm.raw_full[s]), 1);
+        mbar_init(smem_u32(&sm.raw_empty[s]), 4);
+      }
+      for (int s = 0; s < C::kScaleSlots; ++s) {
+        mbar_init(smem_u32(&sm.sc_full[s]), 32);
+        mbar_init(smem_u32(&sm.sc_empty[s]), 4 * nb);
+      }
     }
     for (int i = 0; i < 4; ++i) {   // block i / 2, half i % 2
       mbar_init(smem_u32(&sm.s_full[i]), 1);
@@ -239,16 +302,20 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
   const int64_t row = row0 + g * kPxRows + (warp & 3) * 32 + lane;   // softmax warps: the thread's row
   float m_run = -INFINITY, l_run = 0.f;
   if (warp < 8) {
-    // Q blocks -> shared memory (K-major, 128-byte swizzle), zeros behind the last row
+    // Q blocks -> shared memory (K-major, 128-byte swizzle), zeros behind the last row: 16 threads per row
     const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(P.q) + row0 * kHeadDim;
     const int64_t left = P.rows - row0;
+    const int ch = threadIdx.x & 15;
 #pragma unroll 8
-    for (int t = threadIdx.x; t < 2 * kPxRows * 16; t += 256) {
-      const int r = t >> 4, ch = t & 15;
+    for (int r = threadIdx.x >> 4; r < 2 * kPxRows; r += 16) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r < left) v = *reinterpret_cast<const uint4 *>(qg + (size_t)r * kHeadDim + ch * 8);
-      *reinterpret_cast<uint4 *>(sm.q + (r >> 7) * (kPxRows * 256) + (ch >> 3) * (kPxRows * 128) +
-                                 sw128(r & 127, (ch & 7) * 16)) = v;
+      uint8_t *qb = sm.q + (r >> 7) * (kPxRows * 256);
+      if constexpr (!C::kFp8) {
+        *reinterpret_cast<uint4 *>(qb + (ch >> 3) * (kPxRows * 128) + sw128(r & 127, (ch & 7) * 16)) = v;
+      } else {
+        px_split_q(v, qb, r & 127, ch, P.scale_log2, sm.qscale + r);
+      }
     }
     fence_proxy_async_smem();
     if (g < nb) {   // O = 0: every product accumulates, on the lanes that it concerns
@@ -259,10 +326,11 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
     }
     tc_fence_before();
     asm volatile("bar.arrive 1, 320;" ::: "memory");   // the MMA warps wait for these alone
+    if constexpr (C::kFp8) asm volatile("bar.sync 10, 256;" ::: "memory");   // the row factors
     if (g < nb) {
       // ------------------------------------------------------------ softmax
       const uint32_t s_addr = lane_addr + g * 128, o_addr = lane_addr + 256 + g * 128;
-      const float sc = P.scale_log2;
+      const float sc = C::kFp8 ? sm.qscale[g * kPxRows + (warp & 3) * 32 + lane] : P.scale_log2;
       const float2 sc2 = make_float2(sc, sc);
       const int rl = (warp & 3) * 32 + lane;
       const int my_q = (int)(row / P.n_heads);           // flat query token
@@ -285,11 +353,10 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
         }
         const float *ksc = sm.scale, *vsc = sm.scale;
         if constexpr (C::kFp8) {
-          const int tk = 2 * it, tv = 2 * it + 1;
-          ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[tk % C::kScaleSlots], (tk / C::kScaleSlots) & 1);
-          ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[tv % C::kScaleSlots], (tv / C::kScaleSlots) & 1);
-          ksc += (tk % C::kScaleSlots) * kPxTile;
-          vsc += (tv % C::kScaleSlots) * kPxTile;
+          const int c = it % C::kScaleSlots;
+          ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.sc_full[c], (it / C::kScaleSlots) & 1);
+          ksc += c * 2 * kPxTile;
+          vsc += (c * 2 + 1) * kPxTile;
         }
         if (hi > lo) {
           const bool mine = lo < (warp & 3) * 32 + 32 && hi > (warp & 3) * 32;   // some lane of this warp
@@ -299,9 +366,8 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
             ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.s_full[2 * g + h], c_s & 1);
             tc_fence_after();
             if (h == 0 && own && !C::kFp8 && tile_valid < kPxTile && ok) {   // V rows behind the sequence's last: zero
-              const int tv = 2 * it + 1;
-              ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[tv % C::kSlots], (tv / C::kSlots) & 1);
-              uint8_t *vt = sm.ring + (tv % C::kSlots) * kPxTileBytes;
+              ok = warp_wait_all(P.status, sm.abort_flag, &sm.v_full[C::vs(it)], C::vp(it));
+              uint8_t *vt = sm.v + C::vs(it) * kPxTileBytes;
               for (int e = tile_valid * 16 + (threadIdx.x & 127); e < kPxTile * 16; e += 128)
                 *reinterpret_cast<uint4 *>(vt + (e & 1) * (kPxTile * 128) + (e >> 1) * 16) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
@@ -382,73 +448,87 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
         if (!ok && own) break;
         if constexpr (C::kFp8) {
           __syncwarp();
-          if (lane == 0 && ok) {
-            mbar_arrive(smem_u32(&sm.sc_empty[(2 * it) % C::kScaleSlots]));
-            mbar_arrive(smem_u32(&sm.sc_empty[(2 * it + 1) % C::kScaleSlots]));
-          }
+          if (lane == 0 && ok) mbar_arrive(smem_u32(&sm.sc_empty[it % C::kScaleSlots]));
         }
       }
     }
   } else {
     if (warp == kPxWarpTma) {
       // ------------------------------------------------------------ producer
+      const bool issuer = elect_one();
       int it = 0;
-      for (; it < 2 * n; ++it) {   // K_0, V_0, K_1, V_1, ...
-        const bool own = (it >> 1) >= np, is_v = it & 1;
-        const CUtensorMap *map = own ? (is_v ? &tm.v : &tm.k) : (is_v ? &tm.pv : &tm.pk);
-        const int y = own ? (int)W.y(P) : (tile0 + (it >> 1)) * kPxTile;
-        if constexpr (!C::kFp8) {
-          const int s = it % C::kSlots;
-          if (it >= C::kSlots && !warp_wait_all(P.status, sm.abort_flag, &sm.empty[s], ((it / C::kSlots) & 1) ^ 1)) break;
-          if (lane == 0) {
-            const uint32_t st = smem_u32(sm.ring + s * kPxTileBytes), bar = smem_u32(&sm.full[s]);
-            mbar_arrive_expect_tx(bar, kPxTileBytes);
-            tma_load_2d(st, map, bar, 0, y);
-            tma_load_2d(st + kPxTile * 128, map, bar, 64, y);
-          }
-        } else {
-          const int s = it % C::kRaw, c = it % C::kScaleSlots;
-          if (it >= C::kRaw && !warp_wait_all(P.status, sm.abort_flag, &sm.raw_empty[s], ((it / C::kRaw) & 1) ^ 1)) break;
-          if (lane == 0) {
-            const uint32_t bar = smem_u32(&sm.raw_full[s]);
-            mbar_arrive_expect_tx(bar, kPxRawBytes);
-            tma_load_2d(smem_u32(sm.raw + s * kPxRawBytes), map, bar, 0, y);
-          }
-          if (it >= C::kScaleSlots && !warp_wait_all(P.status, sm.abort_flag, &sm.sc_empty[c], ((it / C::kScaleSlots) & 1) ^ 1)) break;
-          const float *sc = (is_v ? P.v_scale : P.k_scale) + (own ? 0 : P.prefix_start) + y;
-          const int valid = own ? W.valid(P) : P.prefix_len - y;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = u * 32 + lane;
-            const bool in = r < valid;
-            cp_async_4(smem_u32(sm.scale + c * kPxTile + r), sc + (in ? r : 0), in ? 4u : 0u);
-          }
-          cp_async_mbar_arrive(smem_u32(&sm.sc_full[c]));
+      bool ok = true;
+      for (; it < n; ++it) {
+        const bool own = it >= np;
+        const CUtensorMap *mk = own ? &tm.k : &tm.pk, *mv = own ? &tm.v : &tm.pv;
+        const int y = own ? (int)W.y(P) : (tile0 + it) * kPxTile;
+        if (own) W.next(P);
+        const int sk = C::ks(it), sv = C::kFp8 ? it % 2 : C::vs(it);
+        if (it >= 3)
+          ok = warp_wait_all(P.status, sm.abort_flag, &sm.k_empty[sk], C::kp(it) ^ 1);
+        if (!ok) break;
+        if (issuer) {
+          const uint32_t st = smem_u32(sm.k + sk * C::kKBytes), bar = smem_u32(&sm.k_full[sk]);
+          mbar_arrive_expect_tx(bar, C::kKBytes);
+          tma_load_2d(st, mk, bar, 0, y);
+          if (!C::kFp8) tma_load_2d(st + kPxTile * 128, mk, bar, 64, y);
         }
-        if (is_v && own) W.next(P);
+        __syncwarp();
+        if constexpr (C::kFp8) {
+          if (it >= 2) ok = warp_wait_all(P.status, sm.abort_flag, &sm.raw_empty[sv], ((it / 2) & 1) ^ 1);
+        } else {
+          if (it >= 2) ok = warp_wait_all(P.status, sm.abort_flag, &sm.v_empty[sv], C::vp(it) ^ 1);
+        }
+        if (!ok) break;
+        if (issuer) {
+          const uint32_t st = smem_u32(C::kFp8 ? sm.raw + sv * kPxRawBytes : sm.v + sv * kPxTileBytes);
+          const uint32_t bar = smem_u32(C::kFp8 ? &sm.raw_full[sv] : &sm.v_full[sv]);
+          mbar_arrive_expect_tx(bar, C::kKBytes);
+          tma_load_2d(st, mv, bar, 0, y);
+          if (!C::kFp8) tma_load_2d(st + kPxTile * 128, mv, bar, 64, y);
+        }
         __syncwarp();
       }
-      if (it < 2 * n && lane == 0) {   // gave up: the copies in flight land before the CTA ends
-        constexpr int N = C::kFp8 ? C::kRaw : C::kSlots;
-        for (int j = max(0, it - N); j < it; ++j)
-          mbar_wait(smem_u32(C::kFp8 ? &sm.raw_full[j % N] : &sm.full[j % N]), (j / N) & 1);
+      if (!ok) {   // gave up: copies in flight land before the CTA ends (they take microseconds)
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {}
       }
-      if constexpr (C::kFp8) asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+    } else if (C::kFp8 && warp == kPxWarpScale) {
+      // ------------------------------------------------------------ the tiles' scales
+      for (int it = 0; it < n; ++it) {
+        const bool own = it >= np;
+        const int64_t y = own ? W.y(P) : P.prefix_start + (int64_t)(tile0 + it) * kPxTile;
+        const int valid = own ? W.valid(P) : P.prefix_len - (tile0 + it) * kPxTile;
+        if (own) W.next(P);
+        const int c = it % kPxScaleSlots;
+        if (it >= kPxScaleSlots && !warp_wait_all(P.status, sm.abort_flag, &sm.sc_empty[c], ((it / kPxScaleSlots) & 1) ^ 1)) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 32 + lane;
+          const bool in = r < valid;
+          cp_async_4(smem_u32(sm.scale + c * 2 * kPxTile + r), P.k_scale + y + (in ? r : 0), in ? 4u : 0u);
+          cp_async_4(smem_u32(sm.scale + (c * 2 + 1) * kPxTile + r), P.v_scale + y + (in ? r : 0), in ? 4u : 0u);
+        }
+        cp_async_mbar_arrive(smem_u32(&sm.sc_full[c]));
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
     } else if (C::kFp8 && warp >= kPxWarpWiden) {
-      // ------------------------------------------------------------ e4m3 codes -> bf16 tiles
+      // ------------------------------------------------------------ V codes -> bf16 tiles
       // 16 codes per thread and step: eight neighbouring threads take four chunks of two rows, which
       // the swizzle spreads over all banks
       const int t = threadIdx.x - kPxWarpWiden * 32;
-      for (int it = 0; it < 2 * n; ++it) {
-        const int r = it % 2, s = it % C::kSlots;
-        if (!warp_wait_all(P.status, sm.abort_flag, &sm.raw_full[r], (it / 2) & 1)) break;
-        if (it >= C::kSlots && !warp_wait_all(P.status, sm.abort_flag, &sm.empty[s], ((it / C::kSlots) & 1) ^ 1)) break;
-        const bool own = (it >> 1) >= np;
+      for (int it = 0; it < n; ++it) {
+        const int s = it % 2;
+        const bool own = it >= np;
         const int valid = own ? W.valid(P) : kPxTile;   // (the prefix's maps end with it)
-        const uint8_t *src = sm.raw + r * kPxRawBytes;
-        uint8_t *dst = sm.ring + s * kPxTileBytes;
-#pragma unroll 2
+        if (own) W.next(P);
+        if (!warp_wait_all(P.status, sm.abort_flag, &sm.raw_full[s], (it / 2) & 1)) break;
+        if (it >= 2 && !warp_wait_all(P.status, sm.abort_flag, &sm.v_empty[s], ((it / 2) & 1) ^ 1)) break;
+        const uint8_t *src = sm.raw + s * kPxRawBytes;
+        uint8_t *dst = sm.v + s * kPxTileBytes;
+#pragma unroll 4
         for (int u = 0; u < 8; ++u) {
           const int e = u * 128 + t;                     // (row pair, half, row of the pair, chunk)
           const int row = (e >> 4) * 2 + ((e >> 2) & 1), ch = ((e >> 3) & 1) * 4 + (e & 3);
@@ -468,10 +548,9 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&sm.full[s]));
-          mbar_arrive(smem_u32(&sm.raw_empty[r]));
+          mbar_arrive(smem_u32(&sm.v_full[s]));
+          mbar_arrive(smem_u32(&sm.raw_empty[s]));
         }
-        if ((it & 1) && own) W.next(P);
       }
     } else if (warp == kPxWarpMma || warp == kPxWarpMma + 1) {
       // ------------------------------------------------------------ MMA issuers, one warp per block
@@ -480,12 +559,12 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
       const int g2 = warp - kPxWarpMma;
       asm volatile("bar.sync 1, 320;" ::: "memory");   // Q and O are ready
       tc_fence_after();
-      const uint32_t id_s = umma_idesc_bf16(kPxRows, 64);
+      const uint32_t id_s = C::kFp8 ? umma_idesc_e4m3(kPxRows, 64) : umma_idesc_bf16(kPxRows, 64);
       const uint32_t id_o = umma_idesc_bf16_bmn(kPxRows, kHeadDim);
       // operand descriptors: the address field counts 16 bytes
       const uint64_t q_desc = umma_desc_sw128(smem_u32(sm.q) + g2 * (kPxRows * 256), 1024);
-      const uint64_t k_desc = umma_desc_sw128(smem_u32(sm.ring), 1024);
-      const uint64_t v_desc = umma_desc_sw128_mn(smem_u32(sm.ring), kPxTile * 128, 1024);
+      const uint64_t k_desc = umma_desc_sw128(smem_u32(sm.k), 1024);
+      const uint64_t v_desc = umma_desc_sw128_mn(smem_u32(sm.v), kPxTile * 128, 1024);
       const uint32_t s_tmem = tmem + g2 * 128, o_tmem = tmem + 256 + g2 * 128;
       const bool issuer = elect_one();                 // the operands stay warp-uniform
       const int rows = g2 == 0 ? rows_g[0] : rows_g[1];
@@ -507,20 +586,20 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
         // Tiles that do not concern this block go back as they are -- behind the P . V before them, whose
         // slot the ring needs to bring them.
         while (cur < 0 && next < n && nhi <= nlo && ok) {
-          for (int t = 2 * next; t < 2 * next + 2 && ok; ++t) {
-            ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[t % C::kSlots], (t / C::kSlots) & 1);
-            if (ok && lane == 0) mbar_arrive(smem_u32(&sm.empty[t % C::kSlots]));
-          }
+          ok = warp_wait_all(P.status, sm.abort_flag, &sm.k_full[C::ks(next)], C::kp(next));
+          if (ok && lane == 0) mbar_arrive(smem_u32(&sm.k_empty[C::ks(next)]));
+          ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.v_full[C::vs(next)], C::vp(next));
+          if (ok && lane == 0) mbar_arrive(smem_u32(&sm.v_empty[C::vs(next)]));
           ++next;
           look();
         }
         const bool more = next < n && nhi > nlo;
         if (!ok || (!more && cur < 0)) break;
-        const int sk = (2 * next) % C::kSlots, tv = 2 * cur + 1, sv = tv % C::kSlots;
-        const uint64_t kd = k_desc + (uint32_t)(sk * (kPxTileBytes >> 4));
+        const int sk = C::ks(next), sv = C::vs(max(cur, 0));
+        const uint64_t kd = k_desc + (uint32_t)(sk * (C::kKBytes >> 4));
         const uint64_t vd = v_desc + (uint32_t)(sv * (kPxTileBytes >> 4));
-        if (more) ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[sk], ((2 * next) / C::kSlots) & 1);
-        if (ok && cur >= 0) ok = warp_wait_all(P.status, sm.abort_flag, &sm.full[sv], (tv / C::kSlots) & 1);
+        if (more) ok = warp_wait_all(P.status, sm.abort_flag, &sm.k_full[sk], C::kp(next));
+        if (ok && cur >= 0) ok = warp_wait_all(P.status, sm.abort_flag, &sm.v_full[sv], C::vp(cur));
         if (!ok) break;
         const bool every = lo == 0 && hi == kPxRows;
         uint32_t off[4];       // lanes left as they are
@@ -550,8 +629,11 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
             if (more) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
+                // bf16: 16 dims a step, two boxes of 64; e4m3: 32 dims a step, the hi and then the lo terms
                 const uint32_t o = ((k >> 2) * (kPxTile * 128) + (k & 3) * 32) >> 4;
-                umma_bf16(s_tmem + h * 64, q_desc + o, kd + o + h * (64 * 128 >> 4), id_s, k > 0);
+                const uint32_t kof = h * (64 * 128 >> 4) + (C::kFp8 ? (k & 3) * 2 : o);
+                if (C::kFp8) umma_e4m3(s_tmem + h * 64, q_desc + o, kd + kof, id_s, k > 0);
+                else umma_bf16(s_tmem + h * 64, q_desc + o, kd + kof, id_s, k > 0);
               }
               umma_commit(smem_u32(&sm.s_full[2 * g2 + h]));
             }
@@ -560,8 +642,8 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
         }
         if (!ok) break;
         if (issuer) {          // the slots are free once these products are done
-          if (cur >= 0) umma_commit(smem_u32(&sm.empty[sv]));
-          if (more) umma_commit(smem_u32(&sm.empty[sk]));
+          if (cur >= 0) umma_commit(smem_u32(&sm.v_empty[sv]));
+          if (more) umma_commit(smem_u32(&sm.k_empty[sk]));
         }
         __syncwarp();
         cur = -1;

@@ -1676,7 +1676,8 @@ hs2_status hs2_prefix_attn(const hs2_kv_view *kv, int64_t prefix_start, int32_t 
     st = encode_2d(i == 0 ? &pm.pk : i == 1 ? &pm.pv : i == 2 ? &pm.k : &pm.v,
                    bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, bf16 ? 2 : 1,
                    own ? base : base + prefix_start * row_bytes, rows, 128, 128, kPrefixTile, bf16 ? 64 : 128,
-                   bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, own ? "K/V" : "prefix K/V");
+                   bf16 || !(i & 1) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,   // V codes: widened
+                   own ? "K/V" : "prefix K/V");
     if (st != HS2_OK) return st;
   }
   PrefixParams pp;
