@@ -44,6 +44,7 @@ constexpr int kPxRows = 128;                       // (query, head) rows per blo
 constexpr int kPxTileBytes = kPxTile * 256;        // two [128][128 B] swizzled dim blocks
 constexpr int kPxRawBytes = kPxTile * 128;         // a tile of codes
 constexpr int kPxScaleSlots = 4;                   // e4m3: tiles whose scales are in flight
+constexpr int kPxOutRow = 528, kPxOutWarp = 32 * kPxOutRow;   // a warp's rows of O on their way out: 512 bytes + 16
 constexpr float kPxLazy = 8.f;
 constexpr int kPxWarpMma = 8, kPxWarpTma = 10, kPxWarpScale = 11, kPxWarpWiden = 12;   // MMA: a warp per block
 constexpr uint32_t kPxCols = 512;                  // S/P at 0 and 128, O at 256 and 384
@@ -63,7 +64,8 @@ struct PxCfg {
   static constexpr size_t kScaleOff = kRawOff + (size_t)kRaw * kPxRawBytes;
   static constexpr size_t kQScaleOff = kScaleOff + (kFp8 ? (size_t)kScaleSlots * 2 * kPxTile * 4 : 0);
   static constexpr size_t kBarOff = kQScaleOff + (kFp8 ? 2 * kPxRows * 4 : 0);
-  static constexpr int kBars = 2 * 5 + 2 * 2 + 2 * 2 + 2 * 4 + 4 + 4 + 2 + 2;
+  static constexpr int kBars = 2 * 5 + 2 * 2 + 2 * 2 + 2 * 4 + 4 + 4 + 2 + 2 + 1;
+  static_assert(8 * kPxOutWarp <= kScaleOff, "the results leave through the tiles' memory");
   static constexpr size_t kBytes = 1024 + kBarOff + kBars * 8 + 16;
   static_assert(kBytes <= 227 * 1024, "shared memory");
   // slot and parity of tile it's K and V
@@ -79,7 +81,7 @@ struct PxSmem {
   uint8_t *q, *k, *v, *raw;
   float *scale, *qscale;      // [slot][K, V][128]; [row]: c log2 e and the row's power of two
   uint64_t *k_full, *k_empty, *v_full, *v_empty;   // bf16: the same ring
-  uint64_t *raw_full, *raw_empty, *sc_full, *sc_empty, *s_full, *p_full, *o_done, *done;
+  uint64_t *raw_full, *raw_empty, *sc_full, *sc_empty, *s_full, *p_full, *o_done, *done, *q_full;
   uint32_t *tmem_base;
   volatile int *abort_flag;
   __device__ explicit PxSmem(uint8_t *p) {
@@ -101,7 +103,8 @@ struct PxSmem {
     p_full = s_full + 4;
     o_done = p_full + 4;
     done = o_done + 2;
-    tmem_base = reinterpret_cast<uint32_t *>(done + 2);
+    q_full = done + 2;
+    tmem_base = reinterpret_cast<uint32_t *>(q_full + 1);
     abort_flag = reinterpret_cast<volatile int *>(tmem_base + 1);
   }
 };
@@ -276,10 +279,12 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
     mbar_init(smem_u32(&sm.o_done[1]), 1);
     mbar_init(smem_u32(&sm.done[0]), 1);
     mbar_init(smem_u32(&sm.done[1]), 1);
+    mbar_init(smem_u32(&sm.q_full[0]), 1);
     *sm.abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == kPxWarpTma && lane == 0) {
+    prefetch_tensormap(&tm.q);
     prefetch_tensormap(&tm.pk);
     prefetch_tensormap(&tm.pv);
     prefetch_tensormap(&tm.k);
@@ -302,22 +307,24 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
   const int64_t row = row0 + g * kPxRows + (warp & 3) * 32 + lane;   // softmax warps: the thread's row
   float m_run = -INFINITY, l_run = 0.f;
   if (warp < 8) {
-    // Q blocks -> shared memory (K-major, 128-byte swizzle), zeros behind the last row: 16 threads per row
-    const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(P.q) + row0 * kHeadDim;
-    const int64_t left = P.rows - row0;
-    const int ch = threadIdx.x & 15;
-#pragma unroll 8
-    for (int r = threadIdx.x >> 4; r < 2 * kPxRows; r += 16) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < left) v = *reinterpret_cast<const uint4 *>(qg + (size_t)r * kHeadDim + ch * 8);
-      uint8_t *qb = sm.q + (r >> 7) * (kPxRows * 256);
-      if constexpr (!C::kFp8) {
-        *reinterpret_cast<uint4 *>(qb + (ch >> 3) * (kPxRows * 128) + sw128(r & 127, (ch & 7) * 16)) = v;
-      } else {
-        px_split_q(v, qb, r & 127, ch, P.scale_log2, sm.qscale + r);
+    if constexpr (C::kFp8) {   // Q blocks -> shared memory: 16 threads per row, all loads first
+      const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(P.q) + row0 * kHeadDim;
+      const int64_t left = P.rows - row0;
+      const int ch = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+      uint4 v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        const int r = r0 + 16 * i;
+        if (r < left) v[i] = *reinterpret_cast<const uint4 *>(qg + (size_t)r * kHeadDim + ch * 8);
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = r0 + 16 * i;
+        px_split_q(v[i], sm.q + (r >> 7) * (kPxRows * 256), r & 127, ch, P.scale_log2, sm.qscale + r);
+      }
+      fence_proxy_async_smem();
     }
-    fence_proxy_async_smem();
     if (g < nb) {   // O = 0: every product accumulates, on the lanes that it concerns
       const uint32_t zero[32] = {};
 #pragma unroll
@@ -456,9 +463,15 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
     if (warp == kPxWarpTma) {
       // ------------------------------------------------------------ producer
       const bool issuer = elect_one();
-      int it = 0;
       bool ok = true;
-      for (; it < n; ++it) {
+      if (!C::kFp8 && issuer) {   // Q (K-major, 128-byte swizzle; rows behind the last read as zero)
+        mbar_arrive_expect_tx(smem_u32(&sm.q_full[0]), nb * kPxRows * 256);
+        for (int i = 0; i < 2 * nb; ++i)
+          tma_load_2d(smem_u32(sm.q) + i * (kPxRows * 128), &tm.q, smem_u32(&sm.q_full[0]), (i & 1) * 64,
+                      (int)row0 + (i >> 1) * kPxRows);
+      }
+      __syncwarp();
+      for (int it = 0; it < n; ++it) {
         const bool own = it >= np;
         const CUtensorMap *mk = own ? &tm.k : &tm.pk, *mv = own ? &tm.v : &tm.pv;
         const int y = own ? (int)W.y(P) : (tile0 + it) * kPxTile;
@@ -569,6 +582,7 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
       const bool issuer = elect_one();                 // the operands stay warp-uniform
       const int rows = g2 == 0 ? rows_g[0] : rows_g[1];
       bool ok = g2 < nb;
+      if (!C::kFp8) ok = ok && warp_wait_all(P.status, sm.abort_flag, &sm.q_full[0], 0);
       int cur = -1, lo = 0, hi = 0;                    // tile of P . V and its lanes; none yet
       int next = 0, nlo = 0, nhi = 0;                  // tile of S, if it concerns this block, and its lanes
       int used = 0;                                    // tiles that concerned this block
@@ -674,27 +688,33 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
     const bool some = m_run != -INFINITY || l_run != 0.f;   // a row may see nothing in this range
     const float inv = some ? 1.f / l_run : 0.f;
     const bool whole = P.n_splits == 1;
-    float *part = P.part_o + ((int64_t)split * P.rows + row) * kHeadDim;
+    // through shared memory (the tiles are done with), a warp's 32 rows at a time, so that rows leave
+    // in one piece: a thread storing its own row took 6 us
+    uint8_t *mem = sm.q + warp * kPxOutWarp;
 #pragma unroll 1
     for (int c = 0; c < 128; c += 32) {
       float v[32];
-      tmem_ld32(lane_addr + 256 + g * 128 + c, v);
-      tmem_wait_ld();
+      tmem_ld32_issue(lane_addr + 256 + g * 128 + c, v);
+      tmem_wait_ld32(v);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= inv;
-      if (row >= P.rows) continue;
-      if (!whole || P.out_f32) {
-        float *o = whole ? static_cast<float *>(P.out) + row * kHeadDim : part;
-#pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<float4 *>(o + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-      } else {
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(P.out) + row * kHeadDim;
-#pragma unroll
-        for (int i = 0; i < 32; i += 8)
-          *reinterpret_cast<uint4 *>(o + c + i) =
-              make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
-                         pack_bf16(v[i + 6], v[i + 7]));
+      for (int i = 0; i < 32; i += 4)
+        *reinterpret_cast<float4 *>(mem + lane * kPxOutRow + (c + i) * 4) =
+            some ? make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncwarp();
+    const int64_t first = row - lane;                  // the warp's first row
+    const int rows_w = (int)min((int64_t)32, P.rows - first);
+    if (!whole || P.out_f32) {
+      float *o = (whole ? static_cast<float *>(P.out) : P.part_o + (int64_t)split * P.rows * kHeadDim) + first * kHeadDim;
+#pragma unroll 8
+      for (int r = 0; r < rows_w; ++r)
+        *reinterpret_cast<float4 *>(o + r * kHeadDim + lane * 4) = *reinterpret_cast<const float4 *>(mem + r * kPxOutRow + lane * 16);
+    } else {
+      __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(P.out) + first * kHeadDim;
+#pragma unroll 8
+      for (int r = 0; r < rows_w; ++r) {
+        const float4 f = *reinterpret_cast<const float4 *>(mem + r * kPxOutRow + lane * 16);
+        *reinterpret_cast<uint2 *>(o + r * kHeadDim + lane * 4) = make_uint2(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w));
       }
     }
     const float lse = some ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
@@ -714,39 +734,52 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
 // out = sum_j w_j O_j / sum_j w_j, w_j = exp(lse_j - max lse), over the ranges of a row's tiles. One
 // CTA per row: each of its warps sums every kPmWarps-th part, four columns per lane, and the warps'
 // sums meet in shared memory, in warp order.
-constexpr int kPmWarps = 4;
+constexpr int kPmWarps = 8;
 
 __global__ void __launch_bounds__(kPmWarps * 32) prefix_merge_kernel(const __grid_constant__ PrefixParams P) {
   __shared__ float4 s_o[kPmWarps][32];
   __shared__ float s_l[kPmWarps];
+  __shared__ float s_m[kPmWarps];
   __shared__ float s_w[kPxMaxSplits];
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  // every warp finds the maximum itself; warp 0 leaves the parts' log-sum-exps in shared memory
-  float M = -INFINITY;
-  for (int j = lane; j < P.n_splits; j += 32) {
-    const float l = P.part_lse[j * P.rows + row];
-    if (warp == 0) s_w[j] = l;
-    M = fmaxf(M, l);
+  // the parts' log-sum-exps and their maximum; the first parts of O are on their way meanwhile
+  constexpr int kAhead = 4;
+  const float *part = P.part_o + row * kHeadDim + lane * 4;
+  const int64_t stride = P.rows * kHeadDim;
+  float4 v[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int j = warp + i * kPmWarps;
+    v[i] = j < P.n_splits ? *reinterpret_cast<const float4 *>(part + j * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  float M = -INFINITY;
+  if (threadIdx.x < P.n_splits) s_w[threadIdx.x] = M = P.part_lse[threadIdx.x * P.rows + row];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
+  if (lane == 0) s_m[warp] = M;
   __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPmWarps; ++i) M = fmaxf(M, s_m[i]);
+  const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int j = warp; j < P.n_splits; j += kPmWarps) {
+  const auto add = [&](int j, const float4 &x) {
     const float w = expf(s_w[j] - ref);
-    const float4 v = *reinterpret_cast<const float4 *>(P.part_o + (j * P.rows + row) * kHeadDim + lane * 4);
     L += w;
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
-  }
+    o.x = fmaf(w, x.x, o.x);
+    o.y = fmaf(w, x.y, o.y);
+    o.z = fmaf(w, x.z, o.z);
+    o.w = fmaf(w, x.w, o.w);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (warp + i * kPmWarps < P.n_splits) add(warp + i * kPmWarps, v[i]);
+#pragma unroll 4
+  for (int j = warp + kAhead * kPmWarps; j < P.n_splits; j += kPmWarps)
+    add(j, *reinterpret_cast<const float4 *>(part + j * stride));
   s_o[warp][lane] = o;
   if (lane == 0) s_l[warp] = L;
   __syncthreads();

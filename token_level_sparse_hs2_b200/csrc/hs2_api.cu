@@ -1680,6 +1680,9 @@ hs2_status hs2_prefix_attn(const hs2_kv_view *kv, int64_t prefix_start, int32_t 
                    own ? "K/V" : "prefix K/V");
     if (st != HS2_OK) return st;
   }
+  if (bf16 && (st = encode_2d(&pm.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, F.rows, 128, 128, kPrefixTile, 64,
+                              CU_TENSOR_MAP_SWIZZLE_128B, "q")) != HS2_OK)
+    return st;
   PrefixParams pp;
   memset(&pp, 0, sizeof pp);
   for (int b = 0; b < kv->batch; ++b) {

@@ -201,7 +201,7 @@ cudaError_t launch_gemm_fp8_tokens(int tokens, const GemmMaps &tm, const GemmPar
 cudaError_t launch_gemm_fp8_pair(const GemmMaps &tm, const GemmParams &p, int pairs, cudaStream_t s);
 
 // Attention of a batch whose sequences share a prefix.
-constexpr int kPxMaxSplits = 148;   // ranges of a row's tiles, at most
+constexpr int kPxMaxSplits = 148;   // ranges of a row's tiles, at most (a thread each in the merge)
 struct PrefixParams {
   SeqTable seq;               // start, len: the sequences' own rows
   int32_t n_q, n_heads;
@@ -219,6 +219,7 @@ struct PrefixParams {
   uint32_t *status;           // cleared by the first CTA
 };
 struct PrefixMaps {
+  CUtensorMap q;              // [rows, 128], boxes of 128 rows x 64 (bf16 caches)
   CUtensorMap pk, pv;         // the prefix's rows alone; boxes of 128 rows x 128 bytes
   CUtensorMap k, v;           // the whole cache
 };
