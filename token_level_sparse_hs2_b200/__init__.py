@@ -137,13 +137,15 @@ def default_scale(head_dim: int = HEAD_DIM) -> float:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
+    """The cudaStream_t of `stream`, or of the current device's current stream (asked for as the bare
+    handle: building torch's Stream object takes 3 us, as long as a launch)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 class KvCache:
@@ -359,28 +361,32 @@ def kv_bridge(cache: KvCache, hidden, w_kv, workspace, stream=None):
 
 # ---------------------------------------------------------------- operators around the block
 
-def _matrix(name: str, t: torch.Tensor, dtypes, shape=None) -> torch.Tensor:
-    """A [rows, cols] tensor with unit column stride and (if given) this shape."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name} must be 2-D with contiguous rows")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    return t
-
-
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
 _WIDE = (torch.bfloat16, torch.float32)
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements between rows; a single row's stride is its length rounded up to 16."""
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+def _matrix(name: str, t: torch.Tensor, dtypes, shape=None, pad: int = 16) -> int:
+    """Checks a [rows, cols] tensor with unit column stride and (if given) this shape; returns the
+    elements between rows (a single row's are its length rounded up to `pad`)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}")
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
+        raise ValueError(f"{name} must be {'2-D' if shape is None else list(shape)}, not {list(size)}")
+    ld, unit = t.stride()
+    if unit != 1 and size[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return ld if size[0] > 1 else -(-size[1] // pad) * pad
 
 
-def _scale_ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 4) * 4
+def _here(*tensors) -> None:
+    """Every tensor has to be on the current device, where the kernels run."""
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{device}")
 
 
 def fp8_scales(rows: int, cols: int, block_rows: int = 1, device="cuda") -> torch.Tensor:
@@ -396,58 +402,62 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out
     """Root-mean-square norm with the residual's addition (hs2_rms_norm): h = x + residual,
     residual_out = h, y = h weight / sqrt(mean(h^2) + eps), given as `out` (bf16 or float32)
     and / or as e4m3 `codes` with `scales` (fp8_scales) for each 128 columns of a row."""
-    rows, d = _matrix("x", x, (torch.bfloat16,)).shape
-    if weight.dtype not in _WIDE or tuple(weight.shape) != (d,) or not weight.is_contiguous():
+    x_ld = _matrix("x", x, _BF16)
+    shape = x.shape
+    rows, d = shape
+    if weight.dtype not in _WIDE or weight.shape != (d,) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous bf16 or float32 [d] tensor")
-    if (residual is None) != (residual_out is None):
-        raise ValueError("residual and residual_out: both or neither")
-    if residual is not None:
-        _matrix("residual", residual, _WIDE, (rows, d))
-        _matrix("residual_out", residual_out, (residual.dtype,), (rows, d))
-        if _row_stride(residual) != _row_stride(residual_out):
+    res_ld = out_ld = codes_ld = scale_ld = res_type = out_type = 0
+    if residual is not None and residual_out is not None:
+        res_type = _out_dtype(residual)
+        res_ld = _matrix("residual", residual, _WIDE, shape)
+        if _matrix("residual_out", residual_out, (residual.dtype,), shape) != res_ld:
             raise ValueError("residual and residual_out must have one row stride")
+    elif residual is not None or residual_out is not None:
+        raise ValueError("residual and residual_out: both or neither")
     if out is not None:
-        _matrix("out", out, _WIDE, (rows, d))
-    if (codes is None) != (scales is None):
+        out_type = _out_dtype(out)
+        out_ld = _matrix("out", out, _WIDE, shape)
+    if codes is not None and scales is not None:
+        codes_ld = _matrix("codes", codes, _CODES, shape)
+        scale_ld = _matrix("scales", scales, _F32, (-(-d // 128), rows), 4)
+    elif codes is not None or scales is not None:
         raise ValueError("codes and scales: both or neither")
-    if codes is not None:
-        _matrix("codes", codes, _CODES, (rows, d))
-        _matrix("scales", scales, (torch.float32,), (-(-d // 128), rows))
-    _check(lib().hs2_rms_norm(
-        rows, d, _ptr(x), _row_stride(x), _ptr(residual), _ptr(residual_out),
-        OUT_BF16 if residual is None else _out_dtype(residual),
-        0 if residual is None else _row_stride(residual), _ptr(weight), _out_dtype(weight), eps,
-        _ptr(out), OUT_BF16 if out is None else _out_dtype(out),
-        0 if out is None else _row_stride(out), _ptr(codes),
-        0 if codes is None else _row_stride(codes), _ptr(scales),
-        0 if scales is None else _scale_ld(scales), _stream(stream)))
+    _here(x, weight, residual, residual_out, out, codes, scales)
+    _check(lib().hs2_rms_norm(rows, d, x.data_ptr(), x_ld, _ptr(residual), _ptr(residual_out), res_type,
+                              res_ld, weight.data_ptr(), _out_dtype(weight), eps, _ptr(out), out_type,
+                              out_ld, _ptr(codes), codes_ld, _ptr(scales), scale_ld, _stream(stream)))
 
 
 def fp8_quantize(x, codes, scales, block_rows: int = 1, stream=None):
     """e4m3 codes and scales of the bf16 matrix x (hs2_fp8_quantize): block_rows 1 gives each row
     its own scales (activations), 128 one scale for each 128 x 128 block (weights)."""
-    rows, cols = _matrix("x", x, (torch.bfloat16,)).shape
-    _matrix("codes", codes, _CODES, (rows, cols))
-    _matrix("scales", scales, (torch.float32,), (-(-cols // 128), -(-rows // max(block_rows, 1))))
-    _check(lib().hs2_fp8_quantize(rows, cols, _ptr(x), _row_stride(x), block_rows, _ptr(codes),
-                                  _row_stride(codes), _ptr(scales), _scale_ld(scales),
-                                  _stream(stream)))
+    x_ld = _matrix("x", x, _BF16)
+    rows, cols = x.shape
+    codes_ld = _matrix("codes", codes, _CODES, x.shape)
+    scale_ld = _matrix("scales", scales, _F32, (-(-cols // 128), -(-rows // max(block_rows, 1))), 4)
+    _here(x, codes, scales)
+    _check(lib().hs2_fp8_quantize(rows, cols, x.data_ptr(), x_ld, block_rows, codes.data_ptr(), codes_ld,
+                                  scales.data_ptr(), scale_ld, _stream(stream)))
 
 
 def gemm_fp8(a, a_scale, w, w_scale, out, workspace, stream=None):
     """out = A W^T of e4m3 codes a [m, k] (1 x 128 scales) and w [n, k] (128 x 128 scales), in
     float32, rounded to out's type (hs2_gemm_fp8). workspace: at least 256 bytes."""
-    m, k = _matrix("a", a, _CODES).shape
-    n = _matrix("w", w, _CODES, (w.shape[0], k)).shape[0]
+    a_ld, w_ld = _matrix("a", a, _CODES), _matrix("w", w, _CODES)
+    m, k = a.shape
+    n = w.shape[0]
+    if w.shape[1] != k:
+        raise ValueError(f"a has {k} columns, w {w.shape[1]}")
     kb = -(-k // 128)
-    _matrix("a_scale", a_scale, (torch.float32,), (kb, m))
-    _matrix("w_scale", w_scale, (torch.float32,), (kb, -(-n // 128)))
-    _matrix("out", out, _WIDE, (m, n))
-    _check(lib().hs2_gemm_fp8(m, n, k, _ptr(a), _row_stride(a), _ptr(a_scale), _scale_ld(a_scale),
-                              _ptr(w), _row_stride(w), _ptr(w_scale), _scale_ld(w_scale),
-                              _ptr(out), _out_dtype(out), out.stride(0) if m > 1 else n,
-                              _ptr(workspace), workspace.numel() * workspace.element_size(),
-                              _stream(stream)))
+    a_scale_ld = _matrix("a_scale", a_scale, _F32, (kb, m), 4)
+    w_scale_ld = _matrix("w_scale", w_scale, _F32, (kb, -(-n // 128)), 4)
+    out_ld = _matrix("out", out, _WIDE, (m, n), 1)
+    _here(a, a_scale, w, w_scale, out, workspace)
+    _check(lib().hs2_gemm_fp8(m, n, k, a.data_ptr(), a_ld, a_scale.data_ptr(), a_scale_ld, w.data_ptr(),
+                              w_ld, w_scale.data_ptr(), w_scale_ld, out.data_ptr(), _out_dtype(out),
+                              out_ld, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def prefix_attn_workspace_size(cache: KvCache, prefix_len: int) -> int:
@@ -462,14 +472,15 @@ def prefix_attn(cache: KvCache, prefix_start: int, prefix_len: int, q, out, lse,
     rows [prefix_start, prefix_start + prefix_len), read once for all of them, and go on with
     their own rows, which `cache` describes (hs2_prefix_attn)."""
     scale = default_scale() if scale is None else scale
-    shape = (cache.batch, cache.n_q, cache.n_heads)
+    rows = (cache.batch, cache.n_q, cache.n_heads)
     if q.dtype != torch.bfloat16 or (lse is not None and lse.dtype != torch.float32):
         raise TypeError("q must be bfloat16 and lse float32")
-    for name, t, want in (("q", q, shape + (128,)), ("out", out, shape + (128,)), ("lse", lse, shape)):
-        if t is not None and (tuple(t.shape) != want or not t.is_contiguous()):
+    for name, t, want in (("q", q, rows + (128,)), ("out", out, rows + (128,)), ("lse", lse, rows)):
+        if t is not None and (t.shape != want or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous {list(want)}")
-    _check(lib().hs2_prefix_attn(cache.ref(), prefix_start, prefix_len, _ptr(q), scale, _ptr(out),
-                                 _out_dtype(out), _ptr(lse), _ptr(workspace),
+    _here(q, out, lse, workspace, cache.k, cache.v)
+    _check(lib().hs2_prefix_attn(cache.ref(), prefix_start, prefix_len, q.data_ptr(), scale,
+                                 out.data_ptr(), _out_dtype(out), _ptr(lse), workspace.data_ptr(),
                                  workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace hs2 {
@@ -310,6 +312,20 @@ __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
 }  // namespace hs2
 
 namespace hs2 {
+// Allows `kernel` its dynamic shared memory, once per device: `done` is the caller's mask of devices
+// (a function-local static of the launcher; the call takes about as long as a launch otherwise).
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // Launches `kernel` with programmatic stream serialization allowed (see griddep_wait).
 template <class Kernel, class... Args>
 cudaError_t launch_pdl(Kernel kernel, int grid, int block, size_t smem, cudaStream_t s,

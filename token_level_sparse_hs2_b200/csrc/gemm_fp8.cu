@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(kGtThreads, 1)
 template <int TN>
 cudaError_t launch_gt(const GemmMaps &tm, const GemmParams &p, cudaStream_t s) {
   auto kern = gemm_fp8_tokens_kernel<TN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GtCfg<TN>::kBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, GtCfg<TN>::kBytes, done);
   if (e != cudaSuccess) return e;
   const int grid = p.n_tiles * p.m_tiles * p.split;
   e = p.split > 1 ? launch_pdl_cluster(kern, grid, kGtThreads, GtCfg<TN>::kBytes, p.split, s, tm, p)

@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kGpThreads, 1)
 }  // namespace
 
 cudaError_t launch_gemm_fp8_pair(const GemmMaps &tm, const GemmParams &p, int pairs, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGpBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(gemm_fp8_pair_kernel, kGpBytes, done);
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(gemm_fp8_pair_kernel, 2 * pairs, kGpThreads, kGpBytes, 2, s, tm, p);
 }
