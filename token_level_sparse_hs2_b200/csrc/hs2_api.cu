@@ -1456,6 +1456,7 @@ hs2_status hs2_rms_norm(int64_t rows, int32_t d, const void *x, int64_t x_stride
   np.w = weight;
   np.w_f32 = weight_dtype == HS2_OUT_F32;
   np.eps = eps;
+  np.inv_d = 1.f / (float)d;
   np.out = out;
   np.out_f32 = out_dtype == HS2_OUT_F32;
   np.out_stride = out_stride;
@@ -1463,7 +1464,9 @@ hs2_status hs2_rms_norm(int64_t rows, int32_t d, const void *x, int64_t x_stride
   np.codes_stride = codes_stride;
   np.scales = scales;
   np.scale_ld = scale_ld;
-  st = cuda_check(launch_rms_norm(np, static_cast<cudaStream_t>(stream)), "rms norm");
+  int sms = 0;
+  if ((st = sm_count(&sms)) != HS2_OK) return st;
+  st = cuda_check(launch_rms_norm(np, sms, static_cast<cudaStream_t>(stream)), "rms norm");
   return st == HS2_OK ? ok() : st;
 }
 

@@ -153,7 +153,7 @@ struct NormParams {
   int64_t res_stride;
   const void *w;              // [d] bf16 or fp32
   int32_t w_f32;
-  float eps;
+  float eps, inv_d;           // inv_d: 1 / d
   void *out;                  // [rows, d] bf16 or fp32, or null
   int32_t out_f32;
   int64_t out_stride;
@@ -162,7 +162,7 @@ struct NormParams {
   float *scales;              // [ceil(d / 128), scale_ld]
   int64_t scale_ld;
 };
-cudaError_t launch_rms_norm(const NormParams &p, cudaStream_t s);
+cudaError_t launch_rms_norm(const NormParams &p, int sms, cudaStream_t s);
 
 // e4m3 codes and scales of a bf16 matrix, 1 x 128 or 128 x 128 blocks.
 struct QuantParams {

@@ -22,6 +22,16 @@ __device__ __forceinline__ float fp8_row_scale(float amax) {
   return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
 }
 
+// The same value in three instructions: the corrected reciprocal product again, whose divisor is a
+// constant here (equal to the division for every float32 significand, exponents 2^-100 ... 2^100: a
+// test goes through them).
+__device__ __forceinline__ float fp8_block_scale(float amax) {
+  if (!(amax >= 0x1p-100f && amax <= 0x1p100f)) return fp8_row_scale(amax);
+  constexpr float r = 1.f / 448.f;
+  const float q0 = __fmul_rn(amax, r);
+  return __fmaf_rn(__fmaf_rn(-448.f, q0, amax), r, q0);
+}
+
 // The per-row constant of fp8_quotient: RN(1 / scale), or 0 to divide directly.
 __device__ __forceinline__ float fp8_row_recip(float sc) {
   return (sc >= 0x1p-100f && sc <= 0x1p100f) ? __frcp_rn(sc) : 0.f;
@@ -41,10 +51,23 @@ __device__ __forceinline__ uint32_t fp8_pair(float a, float b, float sc, float r
                                   __NV_SATFINITE, __NV_E4M3);
 }
 
-// eight codes of a block whose scale is sc (rc = fp8_row_recip(sc))
-__device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float sc, float rc) {
-  return make_uint2((fp8_pair(v[0], v[1], sc, rc) & 0xffffu) | (fp8_pair(v[2], v[3], sc, rc) << 16),
-                    (fp8_pair(v[4], v[5], sc, rc) & 0xffffu) | (fp8_pair(v[6], v[7], sc, rc) << 16));
+// eight codes of a block whose scale is sc (rc = fp8_row_recip(sc)); the quotients as in fp8_quotient, two per
+// instruction
+__device__ __forceinline__ uint2 fp8_codes8(const float2 (&v)[4], float sc, float rc) {
+  uint32_t p[4];
+  if (rc != 0.f) {
+    const float2 r2 = make_float2(rc, rc), n2 = make_float2(-sc, -sc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 q0 = fmul2(v[i], r2), e = ffma2(n2, q0, v[i]), q = ffma2(e, r2, q0);
+      p[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[i].x, sc), __fdiv_rn(v[i].y, sc)), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
 }
 
 }  // namespace hs2

@@ -4,10 +4,15 @@
 //
 //   h = x + residual;  residual_out = h;  y = h w / sqrt(mean(h^2) + eps)
 //
-// One CTA per row (several rows per CTA when a row needs fewer than 256 threads): a thread holds
-// kChunks chunks of 8 columns of h in registers, so x and the residual are read once. The sum of
-// squares goes through warp shuffles and one word of shared memory per warp. 16 neighbouring
-// threads hold 128 columns: the maximum that gives their scale takes four shuffles.
+// A CTA has 256 threads or more for a row (or several rows of fewer threads) and, in a long batch, goes
+// from row to row, the next one's x and residual on their way while this one is worked on (32768 x 4096
+// with e4m3 output, 0.96 GB: @@). A thread holds kChunks chunks of 8 columns of h in registers, so x
+// and the residual are read once. The sum of squares goes through warp shuffles and one word of shared memory
+// per warp. 16 neighbouring threads hold 128 columns: the maximum that gives their scale takes
+// four shuffles.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -16,119 +21,175 @@ namespace hs2 {
 
 namespace {
 
-constexpr int kNormMaxThreads = 512;   // threads per row, at most
+constexpr int kNormMaxThreads = 1024;  // threads per row, at most
 
-__device__ __forceinline__ void load8(const void *p, int64_t i, bool f32, float (&v)[8]) {
-  if (f32) {
-    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 8 columns as they lie in memory: bf16 in u[0], float32 in both
+template <bool kF32>
+struct Raw8 {
+  uint4 u[kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void *p, int64_t i) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + i * (kF32 ? 4 : 2));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    for (int k = 0; k < (kF32 ? 2 : 1); ++k) u[k] = q[k];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < (kF32 ? 2 : 1); ++k) u[k] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    if constexpr (kF32) {
+      v[0] = make_float2(__uint_as_float(u[0].x), __uint_as_float(u[0].y));
+      v[1] = make_float2(__uint_as_float(u[0].z), __uint_as_float(u[0].w));
+      v[2] = make_float2(__uint_as_float(u[1].x), __uint_as_float(u[1].y));
+      v[3] = make_float2(__uint_as_float(u[1].z), __uint_as_float(u[1].w));
+    } else {
+      const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
     }
   }
-}
+};
 
-__device__ __forceinline__ void store8(void *p, int64_t i, bool f32, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void *p, int64_t i, bool f32, const float2 (&v)[4]) {
   if (f32) {
     float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   } else {
     *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
   }
 }
 
-// the largest |v| of this thread's 8 columns and its 15 neighbours'
-__device__ __forceinline__ float amax16(const float (&v)[8]) {
+// the largest |v| of this thread's 8 columns
+__device__ __forceinline__ float amax8(const float2 (&v)[4]) {
   float a = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) a = fmax3(a, fabsf(v[j]), fabsf(v[j + 1]));
+  for (int j = 0; j < 4; ++j) a = fmax3(a, fabsf(v[j].x), fabsf(v[j].y));
+  return a;
+}
+
+// ... and of its 15 neighbours'
+__device__ __forceinline__ float amax16(const float2 (&v)[4]) {
+  float a = amax8(v);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   return a;
 }
 
-// blockDim = (threads per row, a multiple of 32; rows per CTA)
-template <int kChunks>
-__global__ void __launch_bounds__(kNormMaxThreads)
+enum { kResNone = 0, kResBf16 = 1, kResF32 = 2 };
+
+// blockDim = (threads per row, 16 or a multiple of 32; rows per CTA). kAhead: the next row is fetched
+// while this one is worked on.
+template <int kChunks, int kRes, bool kWF32, int kMaxThreads, bool kAhead>
+__global__ void __launch_bounds__(kMaxThreads)
     rms_norm_kernel(const __grid_constant__ NormParams P) {
-  __shared__ float s_sum[kNormMaxThreads / 32];
-  const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31;
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = row < P.rows;
-  griddep_launch_dependents();
-  griddep_wait();
-  float h[kChunks][8];
+  __shared__ float s_sum[2][kMaxThreads / 32];
+  const int T = blockDim.x, tid = threadIdx.x, lane = (threadIdx.y * T + tid) & 31;
+  const int warps = T >> 5;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  int64_t left = P.rows - row;                        // rows from this one on (the thread's own)
+  int64_t base_left = P.rows - (int64_t)blockIdx.x * blockDim.y;   // the CTA's
+  bool in_row[kChunks];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int col = (c * T + tid) * 8;
-    if (live && col < P.d) {
-      load8(P.x, row * P.x_stride + col, false, h[c]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[c][j] = 0.f;
-    }
-  }
-  if (P.res) {
+  for (int c = 0; c < kChunks; ++c) in_row[c] = (c * T + tid) * 8 < P.d;
+  // this thread's first column of the row at hand, in each array
+  constexpr int kRB = kRes == kResF32 ? 4 : 2;
+  const uint8_t *xp = static_cast<const uint8_t *>(P.x) + (row * P.x_stride + tid * 8) * 2;
+  const uint8_t *rp = static_cast<const uint8_t *>(P.res) + (row * P.res_stride + tid * 8) * kRB;
+  uint8_t *rop = static_cast<uint8_t *>(P.res_out) + (row * P.res_stride + tid * 8) * kRB;
+  const int ob = P.out_f32 ? 4 : 2;
+  uint8_t *op = static_cast<uint8_t *>(P.out) + (row * P.out_stride + tid * 8) * ob;
+  uint8_t *cp = P.codes + row * P.codes_stride + tid * 8;
+  float *sp = P.scales + (int64_t)(tid >> 4) * P.scale_ld + row;
+  Raw8<false> xr[kChunks];
+  Raw8<kRes == kResF32> rr[kRes == kResNone ? 1 : kChunks];
+  const auto fetch = [&](bool live) {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int col = (c * T + tid) * 8;
-      if (live && col < P.d) {
-        float r[8];
-        load8(P.res, row * P.res_stride + col, P.res_f32, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[c][j] += r[j];
+      const bool in = live && in_row[c];
+      if (in) xr[c].load(xp, (int64_t)c * T * 8);
+      else xr[c].zero();
+      if (kRes != kResNone) {
+        if (in) rr[c].load(rp, (int64_t)c * T * 8);
+        else rr[c].zero();
       }
     }
+    xp += step * P.x_stride * 2;
+    rp += step * P.res_stride * kRB;
+  };
+  griddep_launch_dependents();
+  griddep_wait();
+  Raw8<kWF32> w[kAhead ? kChunks : 1];
+  if (kAhead) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {   // after every load: residual_out may be residual or x
-      const int col = (c * T + tid) * 8;
-      if (live && col < P.d) store8(P.res_out, row * P.res_stride + col, P.res_f32, h[c]);
+    for (int c = 0; c < kChunks; ++c) {
+      w[c].zero();
+      if (in_row[c]) w[c].load(P.w, (c * T + tid) * 8);
     }
+    fetch(left > 0);
   }
-  float ss = 0.f;
+  for (int turn = 0; base_left > 0; base_left -= step, turn ^= 1) {
+    const bool live = left > 0;
+    if (!kAhead) fetch(live);
+    float2 h[kChunks][4];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c)
+    for (int c = 0; c < kChunks; ++c) {
+      xr[c].get(h[c]);
+      if (kRes != kResNone) {
+        float2 r[4];
+        rr[c].get(r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(h[c][j], h[c][j], ss);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const int warps = T >> 5;
-  if (warps > 1) {
-    float *s = s_sum + threadIdx.y * warps;
-    if (lane == 0) s[tid >> 5] = ss;
-    __syncthreads();
-    ss = 0.f;
-    for (int i = 0; i < warps; ++i) ss += s[i];
-  }
-  const float inv = __frsqrt_rn(__fdiv_rn(ss, (float)P.d) + P.eps);
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int col = (c * T + tid) * 8;
-    const bool in = live && col < P.d;
-    float y[8] = {};
-    if (in) {
-      float w[8];
-      load8(P.w, col, P.w_f32, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = h[c][j] * inv * w[j];
-      if (P.out) store8(P.out, row * P.out_stride + col, P.out_f32, y);
-    }
-    if (P.codes) {
-      const float sc = fp8_row_scale(amax16(y));
-      if (in) {
-        *reinterpret_cast<uint2 *>(P.codes + row * P.codes_stride + col) = fp8_codes8(y, sc, fp8_row_recip(sc));
-        if ((lane & 15) == 0) P.scales[(int64_t)(col >> 7) * P.scale_ld + row] = sc;
+        for (int j = 0; j < 4; ++j) h[c][j] = fadd2(h[c][j], r[j]);
       }
     }
+    left -= step;
+    // (residual_out may be residual or x: the rows ahead are others)
+    if (kAhead && base_left > step) fetch(left > 0);
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      if (kRes != kResNone && live && in_row[c]) store8(rop, (int64_t)c * T * 8, kRes == kResF32, h[c]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2 = ffma2(h[c][j], h[c][j], s2);
+    }
+    float ss = s2.x + s2.y;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (T > 16) ss += __shfl_xor_sync(0xffffffffu, ss, 16);
+    if (warps > 1) {
+      // one barrier a row: a warp that is ahead writes the other half
+      float *s = s_sum[turn] + threadIdx.y * warps;
+      if (lane == 0) s[tid >> 5] = ss;
+      __syncthreads();
+      ss = lane < warps ? s[lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
+    const float inv = __frsqrt_rn(fmaf(ss, P.inv_d, P.eps));
+    const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const bool in = live && in_row[c];
+      if (!kAhead && in) w[0].load(P.w, (c * T + tid) * 8);
+      float2 y[4];
+      w[kAhead ? c : 0].get(y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = in ? fmul2(fmul2(h[c][j], inv2), y[j]) : make_float2(0.f, 0.f);
+      if (P.out && in) store8(op, (int64_t)c * T * 8, P.out_f32, y);
+      if (P.codes) {
+        const float sc = fp8_block_scale(amax16(y));
+        if (in) {
+          *reinterpret_cast<uint2 *>(cp + c * T * 8) = fp8_codes8(y, sc, fp8_row_recip(sc));
+          if ((lane & 15) == 0) sp[(int64_t)(c * (T >> 4)) * P.scale_ld] = sc;
+        }
+      }
+    }
+    rop += step * P.res_stride * kRB;
+    op += step * P.out_stride * ob;
+    cp += step * P.codes_stride;
+    sp += step;
   }
 }
 
@@ -146,24 +207,25 @@ __global__ void __launch_bounds__(kQuThreads)
   const int sub = threadIdx.x & 15;
   griddep_launch_dependents();
   griddep_wait();
-  float v[kQuGroups][8];
+  Raw8<false> raw[kQuGroups];
 #pragma unroll
   for (int u = 0; u < kQuGroups; ++u) {
     const int64_t g = g0 + u * (kQuThreads / 16);
     const int64_t row = g / kb;
     const int col = (int)(g - row * kb) * 128 + sub * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
-    if (g < n && col < P.cols) load8(P.x, row * P.x_stride + col, false, v[u]);
+    if (g < n && col < P.cols) raw[u].load(P.x, row * P.x_stride + col);
+    else raw[u].zero();
   }
 #pragma unroll
   for (int u = 0; u < kQuGroups; ++u) {
     const int64_t g = g0 + u * (kQuThreads / 16);
     const int64_t row = g / kb;
     const int j = (int)(g - row * kb), col = j * 128 + sub * 8;
-    const float sc = fp8_row_scale(amax16(v[u]));
+    float2 v[4];
+    raw[u].get(v);
+    const float sc = fp8_block_scale(amax16(v));
     if (g < n && col < P.cols) {
-      *reinterpret_cast<uint2 *>(P.codes + row * P.codes_stride + col) = fp8_codes8(v[u], sc, fp8_row_recip(sc));
+      *reinterpret_cast<uint2 *>(P.codes + row * P.codes_stride + col) = fp8_codes8(v, sc, fp8_row_recip(sc));
       if (sub == 0) P.scales[(int64_t)j * P.scale_ld + row] = sc;
     }
   }
@@ -179,16 +241,19 @@ __global__ void __launch_bounds__(kQuThreads)
   const int col = jb * 128 + (threadIdx.x & 15) * 8;
   griddep_launch_dependents();
   griddep_wait();
-  float v[8][8];
+  Raw8<false> raw[8];
   float a = 0.f;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     const int64_t row = ib * 128 + u * 16 + (threadIdx.x >> 4);
+    if (row < P.rows && col < P.cols) raw[u].load(P.x, row * P.x_stride + col);
+    else raw[u].zero();
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
-    if (row < P.rows && col < P.cols) load8(P.x, row * P.x_stride + col, false, v[u]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[u][j]));
+  for (int u = 0; u < 8; ++u) {
+    float2 v[4];
+    raw[u].get(v);
+    a = fmaxf(a, amax8(v));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -200,8 +265,10 @@ __global__ void __launch_bounds__(kQuThreads)
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     const int64_t row = ib * 128 + u * 16 + (threadIdx.x >> 4);
+    float2 v[4];
+    raw[u].get(v);
     if (row < P.rows && col < P.cols)
-      *reinterpret_cast<uint2 *>(P.codes + row * P.codes_stride + col) = fp8_codes8(v[u], sc, rc);
+      *reinterpret_cast<uint2 *>(P.codes + row * P.codes_stride + col) = fp8_codes8(v, sc, rc);
   }
   if (threadIdx.x == 0) P.scales[(int64_t)jb * P.scale_ld + ib] = sc;
 }
@@ -224,20 +291,42 @@ cudaError_t launch2d(Kernel kernel, int64_t grid, dim3 block, cudaStream_t s, co
 
 }  // namespace
 
-cudaError_t launch_rms_norm(const NormParams &p, cudaStream_t s) {
+namespace {
+template <int kChunks, int kMaxThreads, bool kAhead = true>
+cudaError_t launch_norm(const NormParams &p, int64_t grid, dim3 block, cudaStream_t s) {
+  const int res = !p.res ? kResNone : p.res_f32 ? kResF32 : kResBf16;
+  const auto with = [&](auto res_c, auto w_c) {
+    return launch2d(rms_norm_kernel<kChunks, decltype(res_c)::value, decltype(w_c)::value, kMaxThreads, kAhead>, grid,
+                    block, s, p);
+  };
+  const auto weights = [&](auto res_c) { return p.w_f32 ? with(res_c, std::true_type{}) : with(res_c, std::false_type{}); };
+  if (res == kResNone) return weights(std::integral_constant<int, kResNone>{});
+  if (res == kResBf16) return weights(std::integral_constant<int, kResBf16>{});
+  return weights(std::integral_constant<int, kResF32>{});
+}
+}  // namespace
+
+cudaError_t launch_rms_norm(const NormParams &p, int sms, cudaStream_t s) {
   const int chunks = (p.d + 7) / 8;
-  int per = 1;
+  // few rows: a chunk per thread, as many threads as that takes; many rows: two chunks per thread, whose loads
+  // are in flight together, and CTAs that go from row to row
+  int per = p.rows <= 2 * sms ? 1 : 2;
+  if (chunks <= 64) per = 1;
   while ((chunks + per - 1) / per > kNormMaxThreads) per *= 2;
-  const int t = ((chunks + per - 1) / per + 31) / 32 * 32;
-  int rows_per = 1;
-  while (t * rows_per * 2 <= 256 && (int64_t)rows_per * 2 <= p.rows / 148) rows_per *= 2;
+  const int t = chunks <= 16 ? 16 : ((chunks + per - 1) / per + 31) / 32 * 32;
+  int rows_per = chunks <= 16 ? 2 : 1;
+  while (t * rows_per * 2 <= 256 && (int64_t)rows_per * 2 <= p.rows / sms) rows_per *= 2;
   const dim3 block(t, rows_per);
-  const int64_t grid = (p.rows + rows_per - 1) / rows_per;
+  const int64_t ctas = (p.rows + rows_per - 1) / rows_per;
+  const int64_t grid = std::min<int64_t>(ctas, (int64_t)sms * std::max(1, 1280 / (t * rows_per)));
+  if (t * rows_per <= 256) {
+    if (per == 1) return launch_norm<1, 256>(p, grid, block, s);
+    return launch_norm<2, 256>(p, grid, block, s);
+  }
   switch (per) {
-    case 1: return launch2d(rms_norm_kernel<1>, grid, block, s, p);
-    case 2: return launch2d(rms_norm_kernel<2>, grid, block, s, p);
-    case 4: return launch2d(rms_norm_kernel<4>, grid, block, s, p);
-    case 8: return launch2d(rms_norm_kernel<8>, grid, block, s, p);
+    case 1: return launch_norm<1, kNormMaxThreads>(p, grid, block, s);
+    case 2: return launch_norm<2, kNormMaxThreads>(p, grid, block, s);
+    case 4: return launch_norm<4, kNormMaxThreads, false>(p, grid, block, s);   // 64 registers a thread
   }
   return cudaErrorInvalidValue;
 }
