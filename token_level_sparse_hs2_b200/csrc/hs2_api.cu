@@ -1560,7 +1560,9 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
   gp.n_tiles = pair ? (n + 255) / 256 : (n + 127) / 128;
   gp.m_tiles = pair ? (int32_t)((m + 255) / 256) : (int32_t)((m + tokens - 1) / tokens);
   const int64_t tiles = (int64_t)gp.n_tiles * gp.m_tiles;
-  gp.split = pair ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({8, gp.kb, sms / std::max<int64_t>(1, tiles)}));
+  // the blocks along k are shared out while the CTAs fit the chip (two per SM for 32 tokens)
+  const int64_t slots = (int64_t)sms * (tokens == 32 ? 2 : 1);
+  gp.split = pair ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({8, gp.kb, slots / std::max<int64_t>(1, tiles)}));
   if (tiles * gp.split > INT32_MAX) return fail(HS2_ERR_UNSUPPORTED, "too many output tiles");
   GemmMaps tm;
   memset(&tm, 0, sizeof tm);
