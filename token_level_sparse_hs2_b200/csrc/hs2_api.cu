@@ -1516,6 +1516,46 @@ hs2_status encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem, const
 }
 }  // namespace
 
+namespace {
+struct GemmChoice {
+  bool pair = false;
+  int tokens = 128, split = 1;
+};
+
+// The tile and the split along k with the least estimated time, in hundredths of a microsecond. Measured
+// (one B200, weights larger than L2, k = 2048 ... 16384): a tile of 128 features x 32 / 64 / 128 tokens takes
+// 4.0 / 7.4 / 8.3 us and, for each block of 128 along k, 0.40 / 0.36 / 0.40 us (32 tokens with two CTAs on
+// an SM: 0.70); a 256 x 256 tile of a CTA pair 3.5 us for the first and 1.8 for each further one, and
+// 0.50 a block. Clusters of more than 4 CTAs do not fill the chip at one CTA per SM (16 of 8 took two waves). So 8 x 16384
+// x 4096 takes 32-token tiles (14.4 us, pairs 20.8), 256 x 16384 x 4096 pairs (21.5 us, 128-token tiles 40.3),
+// 256 x 4096 x 4096 128-token tiles (14.9 us, pairs 19.5).
+GemmChoice choose_gemm(int64_t m, int n, int kb, int sms) {
+  GemmChoice best;
+  best.pair = true;
+  const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  const int64_t rounds = (pair_tiles + sms / 2 - 1) / (sms / 2);
+  int64_t least = rounds * (kb * 50 + 180) + 170;
+  const int64_t n_tiles = (n + 127) / 128;
+  for (int tokens : {32, 64, 128}) {
+    const int64_t tiles = n_tiles * ((m + tokens - 1) / tokens);
+    const int per_sm = tokens == 32 ? 2 : 1, base = tokens == 32 ? 400 : tokens == 64 ? 740 : 830;
+    for (int split = 1; split <= std::min(8, kb); ++split) {
+      const int64_t slots = (int64_t)sms * per_sm * (split <= 2 ? 20 : split <= 4 || per_sm == 2 ? 18 : 15) / 20;
+      const int64_t ctas = tiles * split, waves = (ctas + slots - 1) / slots;
+      const int block = tokens == 64 ? 36 : tokens == 32 && ctas > sms ? 70 : 40;
+      const int64_t cost = waves * ((kb + split - 1) / split * block + base) + (split > 1 ? 50 : 0);
+      if (cost < least) {
+        least = cost;
+        best.pair = false;
+        best.tokens = tokens;
+        best.split = split;
+      }
+    }
+  }
+  return best;
+}
+}  // namespace
+
 hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t lda,
                         const float *a_scale, int64_t a_scale_ld, const void *w, int64_t ldw,
                         const float *w_scale, int64_t w_scale_ld, void *out, int32_t out_dtype,
@@ -1553,16 +1593,13 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
   gp.out_f32 = out_dtype == HS2_OUT_F32;
   gp.ldo = ldo;
   gp.status = static_cast<uint32_t *>(workspace);
-  // pairs of CTAs with 256 x 256 tiles once these fill half the chip
-  const int64_t big = (int64_t)((n + 255) / 256) * ((m + 255) / 256);
-  const bool pair = big >= sms / 4;
-  const int tokens = pair ? 128 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  const GemmChoice ch = choose_gemm(m, n, gp.kb, sms);
+  const bool pair = ch.pair;
+  const int tokens = ch.tokens;
   gp.n_tiles = pair ? (n + 255) / 256 : (n + 127) / 128;
   gp.m_tiles = pair ? (int32_t)((m + 255) / 256) : (int32_t)((m + tokens - 1) / tokens);
   const int64_t tiles = (int64_t)gp.n_tiles * gp.m_tiles;
-  // the blocks along k are shared out while the CTAs fit the chip (two per SM for 32 tokens)
-  const int64_t slots = (int64_t)sms * (tokens == 32 ? 2 : 1);
-  gp.split = pair ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({8, gp.kb, slots / std::max<int64_t>(1, tiles)}));
+  gp.split = ch.split;
   if (tiles * gp.split > INT32_MAX) return fail(HS2_ERR_UNSUPPORTED, "too many output tiles");
   GemmMaps tm;
   memset(&tm, 0, sizeof tm);
