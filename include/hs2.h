@@ -408,8 +408,9 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
  *   lse = log( sum_prefix exp(c q.k_t) + sum_own exp(c q.k_t) ),  out = sum exp(c q.k_t - lse) v_t
  * The prefix's rows are read once for all rows of the batch, not once per sequence. The shared
  * rows may lie anywhere in the cache; kv_rows bounds them too. prefix_len 0: the own rows alone.
- * Cache rows outside the prefix and the sequences are not used, whatever they hold. Both parts
- * are joined from float32. hs2_score_pass takes the lse for the scores of either part (a view of
+ * Cache rows outside the prefix and the sequences are not used, whatever they hold, and one
+ * sequence's rows never touch another's results; with n_q > 1 a non-finite V row of a sequence's
+ * new tokens may reach the queries before it in the same call. The parts are joined from float32. hs2_score_pass takes the lse for the scores of either part (a view of
  * the own rows, and one whose every sequence is the prefix).
  * q: device bf16 [B, n_q, H, 128]; out: device [B, n_q, H, 128] of out_dtype; both 16-byte
  * aligned. lse: device fp32 [B, n_q, H] or NULL. workspace: device, 256-byte aligned, at least

@@ -11,19 +11,28 @@
 //                                running maximum m, the exponentials, the row sum; P is written
 //                                over S as bf16 pairs
 //   O_g += P_g . V_i             tcgen05.mma, A = P (TMEM), B = V tile (MN-major)
-// The blocks alternate on the tensor cores: while block 0's softmax runs, they compute block 1's
-// products. An own tile concerns the lanes of its sequence alone: blocks without such rows skip
-// it, and the product leaves the other lanes of O untouched (its output-lane mask), so a row never
-// meets another sequence's values. The reference maximum only moves when a tile's row maximum
-// exceeds it by more than 8 (P <= 2^8); then the row of O is rescaled in TMEM. P is rounded to
-// bf16 (the tensor cores take no wider operand next to bf16 V; half a step, 2^-8 of each weight,
-// averaged over the keys); m, the sums and O are float32.
+// in two halves of 64 columns with an S buffer each: S of the next tile's half follows the product
+// that frees its buffer, so the softmax warps find it ready. An own tile concerns the lanes of its
+// sequence alone: blocks without such rows skip it, and the product leaves the other lanes of O
+// untouched (its output-lane mask), so a row never meets another sequence's values. The reference
+// maximum only moves when a tile's row maximum exceeds it by more than 8 (P <= 2^8); then the row of
+// O is rescaled in TMEM. P is rounded to bf16 (the tensor cores take no wider operand next to bf16 V;
+// half a step, 2^-8 of each weight, averaged over the keys); m, the sums and O are float32.
+//
+// What bounds it: 4 x 128 queries x 32 heads behind 30,001 rows take 237 us (1,066 TFLOP/s, 0.64 of the
+// measured bf16 rate); the tensor pipe is active 64 % of the time, its operand reads take 61 % of
+// shared memory's cycles (S with 64 columns reads Q for every 64 keys), the special-function unit is
+// busy 64 %: each waits for the others at times, and none alone is the limit. Slower were S in one piece of 128
+// columns without a second buffer (267 us), 16 softmax warps with half the columns each (275 us), one
+// MMA warp for both blocks, and part of the exponentials on the FMA pipe. Few rows behind a long prefix
+// (32 x 1 behind 131,072: 70 us, 0.58 of the rate) add 7 us of set-up and results and the merge's 5.
 //
 // An e4m3 cache (value = scale[t] code): S comes from the cached codes as they are (kind::f8f6f4), the
 // query split into two e4m3 terms after a power of two per row that puts its largest element in
 // [128, 256): hi is q rounded to e4m3, lo the remainder, exact for every element of at least 2^-10 of
 // the row's largest. Four more warps widen the V codes to bf16 (exact). The K scale and the row's power
-// of two multiply S, the V scale the weight before its rounding.
+// of two multiply S, the V scale the weight before its rounding: they and the widening cost 423 us
+// where bf16 takes 237 (without the scales 355).
 //
 // Rows of a tile behind the prefix's or the sequence's last never count, whatever the cache
 // holds there: their columns are masked, and their V rows are zero (the prefix's tensor maps end at its
@@ -171,18 +180,12 @@ template <bool kFp8>
 __device__ __forceinline__ void px_weights(const float (&x)[32], float2 sc2, float2 neg, const float *vsc, float2 &ls,
                                            uint32_t (&pk)[16]) {
 #pragma unroll
-  for (int k = 0; k < 16; k += 2) {
-    const float2 z0 = ffma2(make_float2(x[2 * k], x[2 * k + 1]), sc2, neg);
-    const float2 z1 = ffma2(make_float2(x[2 * k + 2], x[2 * k + 3]), sc2, neg);
-    float2 e0 = make_float2(fast_exp2(z0.x), fast_exp2(z0.y)), e1 = make_float2(fast_exp2(z1.x), fast_exp2(z1.y));
-    ls = fadd2(ls, fadd2(e0, e1));
-    if (kFp8) {
-      const float4 f = *reinterpret_cast<const float4 *>(vsc + 2 * k);
-      e0 = fmul2(e0, make_float2(f.x, f.y));
-      e1 = fmul2(e1, make_float2(f.z, f.w));
-    }
-    pk[k] = pack_bf16(e0.x, e0.y);
-    pk[k + 1] = pack_bf16(e1.x, e1.y);
+  for (int k = 0; k < 16; ++k) {
+    const float2 z = ffma2(make_float2(x[2 * k], x[2 * k + 1]), sc2, neg);
+    float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+    ls = fadd2(ls, e);
+    if (kFp8) e = fmul2(e, *reinterpret_cast<const float2 *>(vsc + 2 * k));
+    pk[k] = pack_bf16(e.x, e.y);
   }
 }
 

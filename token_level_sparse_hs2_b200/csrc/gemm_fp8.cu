@@ -17,6 +17,10 @@
 // tiles than CTAs fit, a cluster of up to 8 CTAs shares a tile, each taking a contiguous range of the
 // blocks; their sums meet in distributed shared memory, each CTA adding a share of the tokens in
 // rank order. Tiles of 32 tokens leave room for two CTAs per SM.
+//
+// What bounds it: with few tokens the stream of weights (8 x 16384 x 16384: 47 us, 5.7 TB/s, 0.87 of
+// measured; 8 x 16384 x 4096, 67 MB: 14.4 us, of which about 4 are start and end), with one small matrix the
+// start and end alone (1 x 256 x 4096: 4.4 us).
 #include "common.cuh"
 #include "internal.h"
 #include "tc05.cuh"
