@@ -148,6 +148,12 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _stream_on(device: int, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device) if torch.cuda.is_initialized() else 0
+
+
 class KvCache:
     """The shared single-head K/V cache of one full-attention layer (device tensors) plus the
     host-side sequence geometry. Sequence b owns rows [kv_start[b], kv_start[b] + kv_len[b]);
@@ -361,42 +367,29 @@ def kv_bridge(cache: KvCache, hidden, w_kv, workspace, stream=None):
 
 # ---------------------------------------------------------------- operators around the block
 
-_BF16 = (torch.bfloat16,)
-_F32 = (torch.float32,)
-_WIDE = (torch.bfloat16, torch.float32)
-_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+_calls_module = None
+
+
+def _calls():
+    """The module of the calls below (raises if it was not built): their checks and marshalling in C++,
+    since in Python they take longer than the kernels of a single token."""
+    global _calls_module
+    if _calls_module is None:
+        lib()
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is missing: build it with "
+                               "`python -m token_level_sparse_hs2_b200.build`") from e
+        _calls_module = module
+    return _calls_module
 
 
 def _device() -> int:
     """The current device, where the kernels run and every tensor has to be."""
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
-
-
-def _refuse(name: str, t: torch.Tensor, dtypes, shape, device: int):
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}")
-    if len(t.shape) != len(shape) or t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
-    raise ValueError(f"{name} must have contiguous rows")
-
-
-def _matrix(name: str, t: torch.Tensor, dtypes, shape, device: int, pad: int = 16) -> int:
-    """Checks a [rows, cols] tensor of this shape with unit column stride on `device`; returns the
-    elements between rows (a single row's are its length rounded up to `pad`)."""
-    if t.dtype not in dtypes or t.shape != shape or t.get_device() != device:
-        _refuse(name, t, dtypes, shape, device)
-    ld, unit = t.stride()
-    if unit != 1 and shape[1] > 1:
-        _refuse(name, t, dtypes, shape, device)
-    return ld if shape[0] > 1 else -(-shape[1] // pad) * pad
-
-
-def _shape2(name: str, t: torch.Tensor):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, not {list(t.shape)}")
-    return t.shape
 
 
 def fp8_scales(rows: int, cols: int, block_rows: int = 1, device="cuda") -> torch.Tensor:
@@ -413,37 +406,8 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out
     residual_out = h, y = h weight / sqrt(mean(h^2) + eps), given as `out` (bf16 or float32)
     and / or as e4m3 `codes` with `scales` (fp8_scales) for each 128 columns of a row."""
     dev = _device()
-    shape = _shape2("x", x)
-    rows, d = shape
-    x_ld = _matrix("x", x, _BF16, shape, dev)
-    if weight.dtype not in _WIDE or weight.shape != (d,) or weight.get_device() != dev:
-        _refuse("weight", weight, _WIDE, (d,), dev)
-    if not weight.is_contiguous():
-        raise ValueError("weight must be contiguous")
-    res_ld = out_ld = codes_ld = scale_ld = res_type = out_type = 0
-    res_p = res_out_p = out_p = codes_p = scales_p = None
-    if residual is not None and residual_out is not None:
-        res_type = OUT_F32 if residual.dtype is torch.float32 else OUT_BF16
-        res_ld = _matrix("residual", residual, _WIDE, shape, dev)
-        if _matrix("residual_out", residual_out, (residual.dtype,), shape, dev) != res_ld:
-            raise ValueError("residual and residual_out must have one row stride")
-        res_p, res_out_p = residual.data_ptr(), residual_out.data_ptr()
-    elif residual is not None or residual_out is not None:
-        raise ValueError("residual and residual_out: both or neither")
-    if out is not None:
-        out_type = OUT_F32 if out.dtype is torch.float32 else OUT_BF16
-        out_ld = _matrix("out", out, _WIDE, shape, dev)
-        out_p = out.data_ptr()
-    if codes is not None and scales is not None:
-        codes_ld = _matrix("codes", codes, _CODES, shape, dev)
-        scale_ld = _matrix("scales", scales, _F32, (-(-d // 128), rows), dev, 4)
-        codes_p, scales_p = codes.data_ptr(), scales.data_ptr()
-    elif codes is not None or scales is not None:
-        raise ValueError("codes and scales: both or neither")
-    st = lib().hs2_rms_norm(rows, d, x.data_ptr(), x_ld, res_p, res_out_p, res_type, res_ld,
-                            weight.data_ptr(), OUT_F32 if weight.dtype is torch.float32 else OUT_BF16,
-                            eps, out_p, out_type, out_ld, codes_p, codes_ld, scales_p, scale_ld,
-                            _stream(stream))
+    st = _calls().rms_norm(x, weight, eps, residual, residual_out, out, codes, scales, dev,
+                           _stream_on(dev, stream))
     if st:
         _check(st)
 
@@ -452,13 +416,7 @@ def fp8_quantize(x, codes, scales, block_rows: int = 1, stream=None):
     """e4m3 codes and scales of the bf16 matrix x (hs2_fp8_quantize): block_rows 1 gives each row
     its own scales (activations), 128 one scale for each 128 x 128 block (weights)."""
     dev = _device()
-    shape = _shape2("x", x)
-    rows, cols = shape
-    x_ld = _matrix("x", x, _BF16, shape, dev)
-    codes_ld = _matrix("codes", codes, _CODES, shape, dev)
-    scale_ld = _matrix("scales", scales, _F32, (-(-cols // 128), -(-rows // max(block_rows, 1))), dev, 4)
-    st = lib().hs2_fp8_quantize(rows, cols, x.data_ptr(), x_ld, block_rows, codes.data_ptr(), codes_ld,
-                                scales.data_ptr(), scale_ld, _stream(stream))
+    st = _calls().fp8_quantize(x, codes, scales, block_rows, dev, _stream_on(dev, stream))
     if st:
         _check(st)
 
@@ -467,21 +425,7 @@ def gemm_fp8(a, a_scale, w, w_scale, out, workspace, stream=None):
     """out = A W^T of e4m3 codes a [m, k] (1 x 128 scales) and w [n, k] (128 x 128 scales), in
     float32, rounded to out's type (hs2_gemm_fp8). workspace: at least 256 bytes."""
     dev = _device()
-    shape = _shape2("a", a)
-    m, k = shape
-    n = _shape2("w", w)[0]
-    kb = -(-k // 128)
-    a_ld = _matrix("a", a, _CODES, shape, dev)
-    w_ld = _matrix("w", w, _CODES, (n, k), dev)
-    a_scale_ld = _matrix("a_scale", a_scale, _F32, (kb, m), dev, 4)
-    w_scale_ld = _matrix("w_scale", w_scale, _F32, (kb, -(-n // 128)), dev, 4)
-    out_ld = _matrix("out", out, _WIDE, (m, n), dev, 1)
-    if workspace.get_device() != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the current device is cuda:{dev}")
-    st = lib().hs2_gemm_fp8(m, n, k, a.data_ptr(), a_ld, a_scale.data_ptr(), a_scale_ld, w.data_ptr(), w_ld,
-                            w_scale.data_ptr(), w_scale_ld, out.data_ptr(),
-                            OUT_F32 if out.dtype is torch.float32 else OUT_BF16, out_ld,
-                            workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    st = _calls().gemm_fp8(a, a_scale, w, w_scale, out, workspace, dev, _stream_on(dev, stream))
     if st:
         _check(st)
 
@@ -498,21 +442,9 @@ def prefix_attn(cache: KvCache, prefix_start: int, prefix_len: int, q, out, lse,
     rows [prefix_start, prefix_start + prefix_len), read once for all of them, and go on with
     their own rows, which `cache` describes (hs2_prefix_attn)."""
     scale = default_scale() if scale is None else scale
-    rows, dev = (cache.batch, cache.n_q, cache.n_heads), _device()
-    full = rows + (128,)
-    for name, t, dtypes, shape in (("q", q, _BF16, full), ("out", out, _WIDE, full), ("lse", lse, _F32, rows)):
-        if t is None and name == "lse":
-            continue
-        if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev:
-            _refuse(name, t, dtypes, shape, dev)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    for name, t in (("k", cache.k), ("v", cache.v), ("workspace", workspace)):
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    st = lib().hs2_prefix_attn(cache.ref(), prefix_start, prefix_len, q.data_ptr(), scale, out.data_ptr(),
-                               OUT_F32 if out.dtype is torch.float32 else OUT_BF16, _ptr(lse),
-                               workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    dev = _device()
+    st = _calls().prefix_attn(ctypes.addressof(cache.view), cache.k, cache.v, prefix_start, prefix_len, q,
+                              scale, out, lse, workspace, dev, _stream_on(dev, stream))
     if st:
         _check(st)
 

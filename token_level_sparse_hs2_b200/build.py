@@ -1,8 +1,9 @@
-"""Builds libhs2.so (the CUDA kernels + C ABI) in-tree for sm_100a with nvcc.
+"""Builds libhs2.so (the CUDA kernels + C ABI) in-tree for sm_100a with nvcc, and the Python module
+_marshal.so (csrc/marshal.cpp: torch tensors to C ABI calls) against it with the host compiler.
 
 Usage: python -m token_level_sparse_hs2_b200.build [--force]
 Object files go to token_level_sparse_hs2_b200/_build/; the library to
-token_level_sparse_hs2_b200/libhs2.so.
+token_level_sparse_hs2_b200/libhs2.so, the module beside it.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhs2.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
@@ -45,6 +47,32 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return res.stderr
 
 
+def _marshal_object(src: str, obj: str) -> None:
+    """Compiles marshal.cpp against torch's headers."""
+    import sysconfig
+
+    import torch
+    inc = [os.path.join(os.path.dirname(torch.__file__), "include"), sysconfig.get_paths()["include"],
+           os.path.join(ROOT, "include")]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", *["-I" + i for i in inc],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-c", src, "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{res.stderr}")
+
+
+def _marshal_link(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:libhs2.so", "-L" + lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{res.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -57,9 +85,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or not os.path.exists(obj) or \
                 os.path.getmtime(obj) < max(os.path.getmtime(src), dep_mtime):
             jobs.append((src, obj))
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
+    msrc, mobj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.cpp.o")
+    m_deps = max(os.path.getmtime(msrc), os.path.getmtime(os.path.join(ROOT, "include", "hs2.h")))
+    m_job = force or not os.path.exists(mobj) or os.path.getmtime(mobj) < m_deps
+    if jobs or m_job:
+        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
+            marshal = ex.submit(_marshal_object, msrc, mobj) if m_job else None
             logs = list(ex.map(lambda j: _compile(j[0], j[1], verbose), jobs))
+            if marshal is not None:
+                marshal.result()
         if verbose:
             for log in logs:
                 sys.stderr.write(log)
@@ -70,6 +104,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr}")
         os.replace(tmp, LIB)
+    if m_job or not os.path.exists(MARSHAL):
+        _marshal_link(mobj)
     return LIB
 
 
