@@ -344,8 +344,8 @@ hs2_status hs2_kv_bridge(const hs2_kv_view *kv, const void *hidden, int32_t d_mo
  * are OCP e4m3fn; a matrix [rows, cols] held in codes has float32 scales for blocks of 1 x 128 or
  * 128 x 128 elements: scales[j * scale_ld + i] belongs to columns [128 j, 128 j + 128) and to row
  * i (1 x 128) or rows [128 i, 128 i + 128) (128 x 128); the last block of columns or rows may be
- * shorter. value = scale * code, scale = max|x| / 448 over the block in float32 (1 for an all-zero
- * block), code = round-to-nearest-even e4m3 of the float32 quotient x / scale: the rule of the
+ * shorter. value = scale * code, scale = max|x| / 448 over the block in float32 (1 where that is
+ * zero), code = round-to-nearest-even e4m3 of the float32 quotient x / scale: the rule of the
  * e4m3 cache rows. scale_ld is a multiple of 4 and at least the number of rows (of blocks of 128
  * rows); scales between that number and scale_ld are never written. Strides count elements
  * between rows. Serving only: there are no backward forms. */
@@ -410,8 +410,9 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
  * rows may lie anywhere in the cache; kv_rows bounds them too. prefix_len 0: the own rows alone.
  * Cache rows outside the prefix and the sequences are not used, whatever they hold, and one
  * sequence's rows never touch another's results; with n_q > 1 a non-finite V row of a sequence's
- * new tokens may reach the queries before it in the same call. The parts are joined from float32. hs2_score_pass takes the lse for the scores of either part (a view of
- * the own rows, and one whose every sequence is the prefix).
+ * new tokens may reach the queries before it in the same call. The parts are joined from
+ * float32. hs2_score_pass takes the lse for the scores of either part (a view of the own rows,
+ * and one whose every sequence is the prefix).
  * q: device bf16 [B, n_q, H, 128]; out: device [B, n_q, H, 128] of out_dtype; both 16-byte
  * aligned. lse: device fp32 [B, n_q, H] or NULL. workspace: device, 256-byte aligned, at least
  * hs2_prefix_attn_workspace_size bytes; its contents on entry do not matter. Asynchronous on

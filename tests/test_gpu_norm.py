@@ -130,6 +130,19 @@ def test_norm_non_finite_rows_stay_their_own():
     assert (y[1, :3] == 0).all() and torch.isnan(y[1, 3]) and torch.isnan(y[2]).all()
 
 
+def test_norm_outputs_near_the_smallest_float32():
+    """y of a few 2^-149 (a weight of 2^-148): out within one step, and blocks whose max|y| / 448 rounds to
+    zero have the scale 1 and codes 0."""
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn((6, 272), generator=g).bfloat16()
+    w = torch.full((272,), 2.0 ** -148)
+    y, out = R.rms_norm(x, w, 1e-6)[1], torch.empty((6, 272), device="cuda")
+    codes, scales = torch.empty((6, 272), dtype=torch.float8_e4m3fn, device="cuda"), hs2.fp8_scales(6, 272)
+    hs2.rms_norm(x.cuda(), w.cuda(), 1e-6, out=out, codes=codes, scales=scales)
+    assert ((out.cpu().double() - y).abs() <= 2.0 ** -149).all()
+    assert (scales == 1).all() and (codes.float() == 0).all()
+
+
 def test_norm_in_place_on_x():
     x, _, w = inputs(33, 512, 1)
     want = R.rms_norm(x, w, 1e-6)[1]

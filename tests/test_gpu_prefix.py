@@ -246,3 +246,44 @@ def test_many_pairs_and_long_prefix():
                 assert ((out[b, i].cpu().double() - ref[b, j]).abs() <= tol).all()
                 want = torch.logsumexp(x, -1)
                 assert ((lse[b, i].cpu().double() - want).abs() <= 1e-4 + 1e-5 * want.abs()).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_overlapping_rows(fp8):
+    """Two sequences with the same own rows, and one whose own rows are the prefix's last."""
+    c = Case([90, 90, 300], 1, 32, 1000, fp8, seed=21)
+    c.first[1] = c.first[0]
+    c.first[2] = c.start + c.prefix - 300
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_later_tokens_key_does_not_reach_earlier_queries(fp8):
+    c = Case([140, 9], 6, 16, 400, fp8, seed=22)
+    want, lse = c.run()
+    row = c.first[0] + 140 - 2                       # the token of query 4
+    if fp8:
+        c.k.view(torch.uint8)[row] = 0x7f
+    else:
+        c.k[row] = float("nan")
+    out, lse2 = c.run()
+    assert torch.equal(out[0, :4], want[0, :4]) and torch.equal(lse2[0, :4], lse[0, :4])
+    assert torch.equal(out[1], want[1]) and not torch.isfinite(out[0, 4:]).any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_behind_32_bit_offsets(fp8):
+    """Prefix and own rows whose elements lie more than 2^31 (bf16) or 2^32 bytes into the cache."""
+    c = Case([50, 300], 1, 32, 1500, fp8, seed=23)
+    want, lse = c.run()
+    at = (1 << 31) // 128 + 77 if not fp8 else (1 << 32) // 128 + 77
+    for name in ("k", "v", "ks", "vs"):
+        small = getattr(c, name)
+        if small is not None:
+            big = torch.empty((at + small.shape[0],) + small.shape[1:], dtype=small.dtype, device="cuda")
+            big[at:] = small
+            setattr(c, name, big)
+    c.start += at
+    c.first = [f + at for f in c.first]
+    out, lse2 = c.run()
+    assert torch.equal(out, want) and torch.equal(lse2, lse)

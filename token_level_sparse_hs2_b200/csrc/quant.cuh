@@ -24,9 +24,12 @@ __device__ __forceinline__ float fp8_row_scale(float amax) {
 
 // The same value in three instructions: the corrected reciprocal product again, whose divisor is a
 // constant here (equal to the division for every float32 significand, exponents 2^-100 ... 2^100: a
-// test goes through them).
+// test goes through them). Of a block so small that the quotient rounds to zero the scale is 1, as of zeros.
 __device__ __forceinline__ float fp8_block_scale(float amax) {
-  if (!(amax >= 0x1p-100f && amax <= 0x1p100f)) return fp8_row_scale(amax);
+  if (!(amax >= 0x1p-100f && amax <= 0x1p100f)) {
+    const float s = fp8_row_scale(amax);
+    return s == 0.f ? 1.f : s;
+  }
   constexpr float r = 1.f / 448.f;
   const float q0 = __fmul_rn(amax, r);
   return __fmaf_rn(__fmaf_rn(-448.f, q0, amax), r, q0);
