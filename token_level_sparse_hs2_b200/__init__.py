@@ -13,6 +13,8 @@ section "KV Reuse and Token-Level Sparse Selection"):
                                window, ascending;
   3. ``sparse_gather_attn`` -- a sparse layer: its own queries over the selected rows only;
   ``block_decode`` chains 1, 2 and n_sparse x 3 on one stream.
+In front of it and behind it: ``rms_norm``, ``fp8_quantize`` and ``gemm_fp8`` (projections in e4m3 with
+block scales), and ``prefix_attn`` for a batch whose sequences share a prefix.
 """
 from __future__ import annotations
 
@@ -25,6 +27,7 @@ import torch
 
 __all__ = ["HS2Error", "KvCache", "lib", "workspace_size", "WS_SCORES", "WS_SELECTION", "full_attn_scores", "topk_select",
            "sparse_gather_attn", "block_decode", "read_device_status", "default_scale",
+           "rms_norm", "fp8_scales", "fp8_quantize", "gemm_fp8", "prefix_attn", "prefix_attn_workspace_size",
            "KV_BF16", "KV_FP8_E4M3", "OUT_BF16", "OUT_F32", "TOPK", "WINDOW"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

@@ -3,8 +3,9 @@
 //
 // These calls are made for single tokens too, where the kernels take 2 to 5 us: reading five or six
 // tensors' types, shapes, strides and devices through Python takes as long again (calls in a loop on a
-// B200: norm of 8 x 4096 9.1 us that way, 3.9 this way; product of 1 x 256 x 4096 9.1 and 5.0). Nothing is computed here and nothing kept. Each function returns the
-// hs2_status of its call; wrong types raise TypeError, wrong shapes, strides and devices ValueError.
+// B200: norm of 8 x 4096 9.1 us that way, 3.9 this way; product of 1 x 256 x 4096 9.1 and 5.0).
+// Nothing is computed here and nothing kept. Each function returns the hs2_status of its call; wrong
+// types raise TypeError, wrong shapes, strides and devices ValueError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
