@@ -287,3 +287,14 @@ def test_rows_behind_32_bit_offsets(fp8):
     c.first = [f + at for f in c.first]
     out, lse2 = c.run()
     assert torch.equal(out, want) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("lens,n_q,prefix,splits", [([150, 100, 90, 500], 80, 700, range(2, 8)), ([60, 50, 45], 40, 3000, range(8, 16)),
+                                                    ([30, 40], 21, 5000, range(16, 32)), ([200, 90], 19, 9001, range(16, 32))])
+def test_many_rows_by_number_of_parts(lens, n_q, prefix, splits):
+    c = Case(lens, n_q, 32, prefix, seed=31)
+    rows = len(lens) * n_q * 32
+    parts = (hs2.prefix_attn_workspace_size(c.cache(), prefix) - 256) // (rows * 129 * 4)
+    assert rows > 8 * 148 and parts in splits
+    c.check(*c.run())
+    c.check(c.run(torch.bfloat16, lse=False)[0], None)

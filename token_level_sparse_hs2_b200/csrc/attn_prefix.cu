@@ -32,7 +32,12 @@
 // [128, 256): hi is q rounded to e4m3, lo the remainder, exact for every element of at least 2^-10 of
 // the row's largest. Four more warps widen the V codes to bf16 (exact). The K scale and the row's power
 // of two multiply S, the V scale the weight before its rounding: they and the widening cost 423 us
-// where bf16 takes 237 (without the scales 355).
+// where bf16 takes 237 (without the scales 355). 32 x 1 queries behind 131,072 rows: 116 us, 106 without the K
+// scales, 109 without the V scales, 101 without the widening, 82 without all three; bf16 66. No pipe is
+// busy for half the time (tensor 39 %, shared memory's loads and stores 41 %, special functions 28 %): a
+// warp's chain through a half tile is longer, 2,300 to 3,500 clocks. A quarter of the columns of four rows per
+// thread, which reads a quarter of the scales, was slower (132 us), as were no turns (130); S in one piece (116),
+// the next barriers tested ahead (118) and other orders of the widened codes (116) changed nothing.
 //
 // Rows of a tile behind the prefix's or the sequence's last never count, whatever the cache
 // holds there: their columns are masked, and their V rows are zero (the prefix's tensor maps end at its
@@ -746,18 +751,22 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
   }
 }
 
-// out = sum_j w_j O_j / sum_j w_j, w_j = exp(lse_j - max lse), over the ranges of a row's tiles. One
-// CTA per row: each of its warps sums every kPmWarps-th part, four columns per lane, and the warps'
-// sums meet in shared memory, in warp order.
-constexpr int kPmWarps = 8;
+// out = sum_j w_j O_j / sum_j w_j, w_j = exp(lse_j - max lse), over the ranges of a row's tiles. kW warps
+// share a row: each sums every kW-th part, four columns per lane, and the warps' sums meet in shared
+// memory, in warp order. Few rows take eight warps each, many one for each four parts or so: with eight, 16,384
+// rows of two parts took 29 us of instructions (4 x 128 queries behind 30,001 rows 234 us in all, now 217).
+constexpr int kPmWarps = 8;           // per CTA
 
+template <int kW>
 __global__ void __launch_bounds__(kPmWarps * 32) prefix_merge_kernel(const __grid_constant__ PrefixParams P) {
-  __shared__ float4 s_o[kPmWarps][32];
+  constexpr int kRows = kPmWarps / kW;
+  __shared__ float4 s_o[kW > 1 ? kPmWarps : 1][32];
   __shared__ float s_l[kPmWarps];
   __shared__ float s_m[kPmWarps];
-  __shared__ float s_w[kPxMaxSplits];
-  const int64_t row = blockIdx.x;
+  __shared__ float s_w[kRows][kW * 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int slot = warp / kW, w0 = warp % kW, t = threadIdx.x % (kW * 32);   // the CTA's row, the warp and thread in it
+  const int64_t row = min((int64_t)blockIdx.x * kRows + slot, P.rows - 1);   // (the last row may be done twice)
   griddep_launch_dependents();
   griddep_wait();
   // the parts' log-sum-exps and their maximum; the first parts of O are on their way meanwhile
@@ -767,22 +776,26 @@ __global__ void __launch_bounds__(kPmWarps * 32) prefix_merge_kernel(const __gri
   float4 v[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
-    const int j = warp + i * kPmWarps;
+    const int j = w0 + i * kW;
     v[i] = j < P.n_splits ? *reinterpret_cast<const float4 *>(part + j * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   float M = -INFINITY;
-  if (threadIdx.x < P.n_splits) s_w[threadIdx.x] = M = P.part_lse[threadIdx.x * P.rows + row];
+  if (t < P.n_splits) s_w[slot][t] = M = P.part_lse[t * P.rows + row];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_m[warp] = M;
-  __syncthreads();
+  if (kW > 1) {
+    if (lane == 0) s_m[warp] = M;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPmWarps; ++i) M = fmaxf(M, s_m[i]);
+    for (int i = 0; i < kW; ++i) M = fmaxf(M, s_m[slot * kW + i]);
+  } else {
+    __syncwarp();
+  }
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const auto add = [&](int j, const float4 &x) {
-    const float w = expf(s_w[j] - ref);
+    const float w = expf(s_w[slot][j] - ref);
     L += w;
     o.x = fmaf(w, x.x, o.x);
     o.y = fmaf(w, x.y, o.y);
@@ -791,22 +804,24 @@ __global__ void __launch_bounds__(kPmWarps * 32) prefix_merge_kernel(const __gri
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
-    if (warp + i * kPmWarps < P.n_splits) add(warp + i * kPmWarps, v[i]);
+    if (w0 + i * kW < P.n_splits) add(w0 + i * kW, v[i]);
 #pragma unroll 4
-  for (int j = warp + kAhead * kPmWarps; j < P.n_splits; j += kPmWarps)
+  for (int j = w0 + kAhead * kW; j < P.n_splits; j += kW)
     add(j, *reinterpret_cast<const float4 *>(part + j * stride));
-  s_o[warp][lane] = o;
-  if (lane == 0) s_l[warp] = L;
-  __syncthreads();
-  if (warp != 0) return;
+  if (kW > 1) {
+    s_o[warp][lane] = o;
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    if (w0 != 0) return;
 #pragma unroll
-  for (int i = 1; i < kPmWarps; ++i) {
-    const float4 v = s_o[i][lane];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
-    L += s_l[i];
+    for (int i = 1; i < kW; ++i) {
+      const float4 x = s_o[warp + i][lane];
+      o.x += x.x;
+      o.y += x.y;
+      o.z += x.z;
+      o.w += x.w;
+      L += s_l[warp + i];
+    }
   }
   const float inv = 1.f / L;
   const int64_t at = row * kHeadDim + lane * 4;
@@ -835,7 +850,15 @@ cudaError_t launch_prefix_attn(int kv_dtype, const PrefixMaps &tm, const PrefixP
 }
 
 cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s) {
-  return launch_pdl(prefix_merge_kernel, (int)p.rows, kPmWarps * 32, 0, s, p);
+  const auto launch = [&](auto kern, int per_row) {
+    const int rows = kPmWarps / per_row;
+    return launch_pdl(kern, (int)((p.rows + rows - 1) / rows), kPmWarps * 32, 0, s, p);
+  };
+  if (p.rows <= 8 * 148) return launch(prefix_merge_kernel<kPmWarps>, kPmWarps);   // at most 8 CTAs an SM
+  if (p.n_splits < 8) return launch(prefix_merge_kernel<1>, 1);
+  if (p.n_splits < 16) return launch(prefix_merge_kernel<2>, 2);
+  if (p.n_splits < 32) return launch(prefix_merge_kernel<4>, 4);
+  return launch(prefix_merge_kernel<kPmWarps>, kPmWarps);
 }
 
 }  // namespace hs2

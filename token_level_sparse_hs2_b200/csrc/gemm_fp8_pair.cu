@@ -12,11 +12,13 @@
 //   warp 8      TMEM owner; in the leader (rank 0) also the MMA issuer for both
 //   warps 10, 11  nothing (the register split goes by groups of four warps)
 //   warps 0..7  epilogue: warp w has lanes 32 (w % 4) .. + 31 and features 128 (w / 4) .. + 127
-// What bounds it: 32768 x 4096 x 4096 takes 505 us (2.18 PFLOP/s, 0.65 of twice the measured bf16 rate; under
-// the power cap of a long run 605 us). A block's products take 512 clocks, the whole step about 980: an
-// accumulator is handed to the epilogue and back through barriers of both CTAs, which takes about 1,000
-// clocks beside its 512 of products and 450 of scaling, and two accumulators (all of TMEM) share that. Handing
-// over halves of 128 features was no faster (515 us).
+// What bounds it: 32768 x 4096 x 4096 takes 505 to 525 us (2.1 to 2.2 PFLOP/s, 0.63 to 0.65 of twice the
+// measured bf16 rate; under the power cap of a long run 600 us). The products and loads alone (accumulators
+// handed back unread) take 411 us, reading and adding them (with a quarter of the products) 441 us: two
+// accumulators, all of TMEM, do not hide one behind the other altogether. The epilogue warps are busy
+// throughout: of about 830 clocks a block 190 go to the barrier, 70 to the first columns, 390 to the rest. No
+// faster were halves of 128 features handed over by themselves (515 against 505 us), 32 columns a load
+// (518 against 523) and the next accumulator's barrier tested, or its first columns fetched, ahead (spills).
 // Persistent over the tiles, features fastest: the CTAs at work share a few token tiles and the
 // weights, which stay in L2. Results pass through shared memory, a 4 KB square per warp, so that
 // rows are stored in 128-byte pieces.
