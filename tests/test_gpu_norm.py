@@ -208,3 +208,21 @@ def test_quantize_of_wide_offsets():
     y = torch.empty((rows, cols), device="cuda")
     hs2.rms_norm(x, torch.ones(cols, device="cuda"), 1e-6, out=y)
     assert (y[-1] - 1).abs().max() < 1e-6 and (y[65536] + 1).abs().max() < 1e-6 and (y != 0).sum() == 2 * cols
+
+
+@pytest.mark.parametrize("rows,d", [(1300, 3584), (1200, 4880), (1190, 8192), (1185, 4112), (400, 8192), (310, 5120), (300, 12288), (150, 9000)])
+@pytest.mark.parametrize("res", [None, torch.bfloat16, torch.float32])
+def test_norm_of_many_wide_rows(rows, d, res):
+    """CTAs that go from row to row, two and four chunks of 8 columns per thread."""
+    x, r, w = inputs(rows, d, rows - d + 9000, res)
+    h, y = R.rms_norm(x, w, 1e-6, r)
+    out = torch.empty((rows, d), dtype=torch.float32, device="cuda")
+    codes, scales = (torch.empty((rows, d), dtype=torch.float8_e4m3fn, device="cuda"), hs2.fp8_scales(rows, d)) if d % 16 == 0 else (None, None)
+    rd = None if r is None else r.cuda()
+    hs2.rms_norm(x.cuda(), w.cuda(), 1e-6, residual=rd, residual_out=rd, out=out, codes=codes, scales=scales)
+    # as in test_norm
+    assert ((out.cpu().double() - y).abs() <= (Y_TOL + HALF[torch.float32]) * y.abs() + 1e-40).all()
+    if rd is not None:
+        assert ((rd.cpu().double() - h).abs() <= (HALF[res] + 2.0 ** -24) * h.abs()).all()
+    if codes is not None:
+        check_codes(y, codes, scales)

@@ -6,8 +6,8 @@
 //
 // A CTA has 256 threads or more for a row (or several rows of fewer threads) and, in a long batch, goes
 // from row to row, the next one's x and residual on their way while this one is worked on (32768 x 4096
-// with e4m3 output, 0.96 GB: 159 us, 5.9 TB/s, 0.90 of measured; 248 us with a CTA per row and no row
-// ahead). A thread holds kChunks chunks of 8 columns of h in registers, so x and the residual are read
+// with e4m3 output, 0.96 GB: 147 us, 6.5 TB/s, the measured copy rate; 248 us with a CTA per row and no
+// row ahead). A thread holds kChunks chunks of 8 columns of h in registers, so x and the residual are read
 // once. The sum of squares goes through warp shuffles and one word of shared memory per warp. 16
 // neighbouring threads hold 128 columns: the maximum that gives their scale takes four shuffles.
 #include <algorithm>
@@ -308,25 +308,33 @@ cudaError_t launch_norm(const NormParams &p, int64_t grid, dim3 block, cudaStrea
 
 cudaError_t launch_rms_norm(const NormParams &p, int sms, cudaStream_t s) {
   const int chunks = (p.d + 7) / 8;
-  // few rows: a chunk per thread, as many threads as that takes; many rows: two chunks per thread, whose loads
-  // are in flight together, and CTAs that go from row to row
-  int per = p.rows <= 2 * sms ? 1 : 2;
-  if (chunks <= 64) per = 1;
-  while ((chunks + per - 1) / per > kNormMaxThreads) per *= 2;
+  // Few rows: a chunk per thread, as many threads as that takes. Many rows: CTAs that go from row to row, two or
+  // four chunks per thread, whose loads are in flight together. Four from 448 chunks on (32768 x 4096 with a
+  // bf16 residual 147 us, 159 with two; x 2560 101 with two, 110 with four), but for a float32 residual, which
+  // takes the registers (8192 x 8192 142 us with two, 167 with four), and from 8 rows an SM (300 x 4096 3.6 us with
+  // two, 4.3 with four). At most 512 threads, since a row ahead takes more than 64 registers (32768 x 5120: 190 us;
+  // 294 with two chunks and 64 registers).
+  int per = p.rows <= 2 * sms || chunks <= 64 ? 1 : chunks >= 448 && p.rows > 8 * sms && !(p.res && p.res_f32) ? 4 : 2;
+  while ((chunks + per - 1) / per > (per == 1 ? kNormMaxThreads : 512) && per < 4) per *= 2;
   const int t = chunks <= 16 ? 16 : ((chunks + per - 1) / per + 31) / 32 * 32;
   int rows_per = chunks <= 16 ? 2 : 1;
-  while (t * rows_per * 2 <= 256 && (int64_t)rows_per * 2 <= p.rows / sms) rows_per *= 2;
+  while (per < 4 && t * rows_per * 2 <= 256 && (int64_t)rows_per * 2 <= p.rows / sms) rows_per *= 2;
   const dim3 block(t, rows_per);
   const int64_t ctas = (p.rows + rows_per - 1) / rows_per;
-  const int64_t grid = std::min<int64_t>(ctas, (int64_t)sms * std::max(1, 1280 / (t * rows_per)));
+  const int threads = per == 4 ? 512 : t * rows_per <= 256 ? 1280 : 704;   // per SM
+  const int64_t grid = std::min<int64_t>(ctas, (int64_t)sms * std::max(1, threads / (t * rows_per)));
   if (t * rows_per <= 256) {
-    if (per == 1) return launch_norm<1, 256>(p, grid, block, s);
-    return launch_norm<2, 256>(p, grid, block, s);
-  }
-  switch (per) {
-    case 1: return launch_norm<1, kNormMaxThreads>(p, grid, block, s);
-    case 2: return launch_norm<2, kNormMaxThreads>(p, grid, block, s);
-    case 4: return launch_norm<4, kNormMaxThreads, false>(p, grid, block, s);   // 64 registers a thread
+    switch (per) {
+      case 1: return launch_norm<1, 256>(p, grid, block, s);
+      case 2: return launch_norm<2, 256>(p, grid, block, s);
+      case 4: return launch_norm<4, 256>(p, grid, block, s);
+    }
+  } else if (t <= 512 && per > 1) {
+    if (per == 2) return launch_norm<2, 512>(p, grid, block, s);
+    return launch_norm<4, 512>(p, grid, block, s);
+  } else if (t <= kNormMaxThreads) {
+    if (per == 1) return launch_norm<1, kNormMaxThreads>(p, grid, block, s);
+    if (per == 4) return launch_norm<4, kNormMaxThreads, false>(p, grid, block, s);   // 64 registers a thread
   }
   return cudaErrorInvalidValue;
 }
