@@ -174,7 +174,8 @@ def test_norm_on_another_stream_and_in_a_graph():
     assert torch.equal(codes.float(), want[0]) and torch.equal(scales, want[1])
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 128), (3, 4096), (127, 144), (128, 128), (130, 2064), (1000, 272)])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 128), (3, 4096), (127, 144), (128, 128), (130, 2064), (1000, 272), (70, 1024),
+                                       (33, 2000), (65, 640), (200, 1152), (67, 512), (9, 16384)])
 @pytest.mark.parametrize("block_rows", [1, 128])
 def test_quantize_matches_the_definition_bit_for_bit(rows, cols, block_rows):
     g = torch.Generator().manual_seed(rows * cols)

@@ -174,6 +174,7 @@ struct QuantParams {
   int64_t codes_stride;
   float *scales;
   int64_t scale_ld;
+  int32_t tile_shift;         // set by the launcher
 };
 cudaError_t launch_fp8_quantize(const QuantParams &p, cudaStream_t s);
 

@@ -198,36 +198,57 @@ __global__ void __launch_bounds__(kMaxThreads)
 constexpr int kQuThreads = 256;
 constexpr int kQuGroups = 4;          // 1 x 128 blocks per 16 threads, all loads first
 
-// 1 x 128 blocks: 16 threads per block, kQuGroups blocks each
+// 1 x 128 blocks: 16 threads per block, kQuGroups blocks each, in rows one below the other. A CTA has 2^tile_shift
+// column blocks of kQuThreads / 16 * kQuGroups >> tile_shift rows. The four maxima meet by a reduction that leaves
+// each with a quarter of the threads, which form its scale and reciprocal and hand them round (32768 x 4096 75
+// us; with every thread reducing and forming all four, and blocks numbered by a division, 97).
 __global__ void __launch_bounds__(kQuThreads)
     fp8_quantize_rows_kernel(const __grid_constant__ QuantParams P) {
-  const int kb = (P.cols + 127) >> 7;
-  const int64_t n = P.rows * kb;
-  const int64_t g0 = (int64_t)blockIdx.x * (kQuThreads / 16 * kQuGroups) + (threadIdx.x >> 4);
-  const int sub = threadIdx.x & 15;
+  static_assert(kQuGroups == 4, "the reduction below");
+  const unsigned ct = (((P.cols + 127) >> 7) + (1 << P.tile_shift) - 1) >> P.tile_shift;
+  const unsigned rt = blockIdx.x / ct;
+  const int grp = threadIdx.x >> 4, sub = threadIdx.x & 15, lane = threadIdx.x & 31;
+  const int j = (int)((blockIdx.x - rt * ct) << P.tile_shift) + (grp & ((1 << P.tile_shift) - 1));
+  const int col = j * 128 + sub * 8;
+  const int step = kQuThreads / 16 >> P.tile_shift;                       // rows between a thread's blocks
+  const int64_t row = (int64_t)rt * step * kQuGroups + (grp >> P.tile_shift);
+  const int left = col < P.cols ? (int)min(P.rows - row, (int64_t)INT32_MAX) : 0;   // rows from its first on
   griddep_launch_dependents();
   griddep_wait();
   Raw8<false> raw[kQuGroups];
 #pragma unroll
   for (int u = 0; u < kQuGroups; ++u) {
-    const int64_t g = g0 + u * (kQuThreads / 16);
-    const int64_t row = g / kb;
-    const int col = (int)(g - row * kb) * 128 + sub * 8;
-    if (g < n && col < P.cols) raw[u].load(P.x, row * P.x_stride + col);
+    if (u * step < left) raw[u].load(P.x, (row + u * step) * P.x_stride + col);
     else raw[u].zero();
+  }
+  float a[kQuGroups];
+#pragma unroll
+  for (int u = 0; u < kQuGroups; ++u) {
+    float2 v[4];
+    raw[u].get(v);
+    a[u] = amax8(v);
+  }
+  const bool b0 = sub & 1, b1 = sub & 2;
+  float k0 = b0 ? a[2] : a[0], k1 = b0 ? a[3] : a[1];                     // blocks 2 b0, 2 b0 + 1
+  k0 = fmaxf(k0, __shfl_xor_sync(0xffffffffu, b0 ? a[0] : a[2], 1));
+  k1 = fmaxf(k1, __shfl_xor_sync(0xffffffffu, b0 ? a[1] : a[3], 1));
+  float k = fmaxf(b1 ? k1 : k0, __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2));   // block 2 b0 + b1
+  k = fmaxf(k, __shfl_xor_sync(0xffffffffu, k, 4));
+  k = fmaxf(k, __shfl_xor_sync(0xffffffffu, k, 8));
+  const float sc = fp8_block_scale(k), rc = fp8_row_recip(sc);
+  if (sub < 4) {
+    const int u = 2 * b0 + b1;
+    const bool any = j * 128 < P.cols && row + u * step < P.rows;
+    if (any) P.scales[(int64_t)j * P.scale_ld + row + u * step] = sc;
   }
 #pragma unroll
   for (int u = 0; u < kQuGroups; ++u) {
-    const int64_t g = g0 + u * (kQuThreads / 16);
-    const int64_t row = g / kb;
-    const int j = (int)(g - row * kb), col = j * 128 + sub * 8;
+    const int src = (lane & 16) + (u >> 1) + 2 * (u & 1);
+    const float s = __shfl_sync(0xffffffffu, sc, src), r = __shfl_sync(0xffffffffu, rc, src);
     float2 v[4];
     raw[u].get(v);
-    const float sc = fp8_block_scale(amax16(v));
-    if (g < n && col < P.cols) {
-      *reinterpret_cast<uint2 *>(P.codes + row * P.codes_stride + col) = fp8_codes8(v, sc, fp8_row_recip(sc));
-      if (sub == 0) P.scales[(int64_t)j * P.scale_ld + row] = sc;
-    }
+    if (u * step < left)
+      *reinterpret_cast<uint2 *>(P.codes + (row + u * step) * P.codes_stride + col) = fp8_codes8(v, s, r);
   }
 }
 
@@ -321,7 +342,9 @@ cudaError_t launch_rms_norm(const NormParams &p, int sms, cudaStream_t s) {
   while (per < 4 && t * rows_per * 2 <= 256 && (int64_t)rows_per * 2 <= p.rows / sms) rows_per *= 2;
   const dim3 block(t, rows_per);
   const int64_t ctas = (p.rows + rows_per - 1) / rows_per;
-  const int threads = per == 4 ? 512 : t * rows_per <= 256 ? 1280 : 704;   // per SM
+  // threads per SM that the registers let stay: a CTA beyond them starts when others have ended (500,000 x 128 with
+  // bf16 residual and codes 72 us, 94 at 1280)
+  const int threads = per == 4 ? 512 : per == 1 ? 1024 : t * rows_per > 256 ? 704 : p.res && p.res_f32 ? 512 : 768;
   const int64_t grid = std::min<int64_t>(ctas, (int64_t)sms * std::max(1, threads / (t * rows_per)));
   if (t * rows_per <= 256) {
     switch (per) {
@@ -343,10 +366,14 @@ cudaError_t launch_fp8_quantize(const QuantParams &p, cudaStream_t s) {
   const int64_t kb = (p.cols + 127) / 128;
   const dim3 block(kQuThreads);
   if (p.block_rows == 1) {
-    const int64_t per = kQuThreads / 16 * kQuGroups;
-    const int64_t grid = (p.rows * kb + per - 1) / per;
+    // the most column blocks per CTA, up to 16, that leave at most an eighth of the threads without one
+    QuantParams q = p;
+    q.tile_shift = 4;
+    while (q.tile_shift && ((kb + (1 << q.tile_shift) - 1) >> q.tile_shift << q.tile_shift) * 8 > kb * 9) --q.tile_shift;
+    const int64_t rows = kQuThreads / 16 * kQuGroups >> q.tile_shift;
+    const int64_t grid = ((kb + (1 << q.tile_shift) - 1) >> q.tile_shift) * ((p.rows + rows - 1) / rows);
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    return launch2d(fp8_quantize_rows_kernel, grid, block, s, p);
+    return launch2d(fp8_quantize_rows_kernel, grid, block, s, q);
   }
   const int64_t grid = (p.rows + 127) / 128 * kb;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
