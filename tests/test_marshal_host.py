@@ -13,6 +13,8 @@ CPU = -1   # device index of a CPU tensor
 
 @pytest.fixture(scope="module")
 def calls():
+    from token_level_sparse_hs2_b200 import build
+    build.build()
     return hs2._calls()
 
 

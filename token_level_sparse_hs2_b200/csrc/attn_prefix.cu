@@ -19,20 +19,20 @@
 // O is rescaled in TMEM. P is rounded to bf16 (the tensor cores take no wider operand next to bf16 V;
 // half a step, 2^-8 of each weight, averaged over the keys); m, the sums and O are float32.
 //
-// What bounds it: 4 x 128 queries x 32 heads behind 30,001 rows take 237 us (1,066 TFLOP/s, 0.64 of the
+// What bounds it: 4 x 128 queries x 32 heads behind 30,001 rows take 217 us (1,160 TFLOP/s, 0.69 of the
 // measured bf16 rate); the tensor pipe is active 64 % of the time, its operand reads take 61 % of
 // shared memory's cycles (S with 64 columns reads Q for every 64 keys), the special-function unit is
 // busy 64 %: each waits for the others at times, and none alone is the limit. Slower were S in one piece of 128
 // columns without a second buffer (267 us), 16 softmax warps with half the columns each (275 us), one
 // MMA warp for both blocks, and part of the exponentials on the FMA pipe. Few rows behind a long prefix
-// (32 x 1 behind 131,072: 70 us, 0.58 of the rate) add 7 us of set-up and results and the merge's 5.
+// (32 x 1 behind 131,072: 68 us, 0.60 of the rate) add 7 us of set-up and results and the merge's 5.
 //
 // An e4m3 cache (value = scale[t] code): S comes from the cached codes as they are (kind::f8f6f4), the
 // query split into two e4m3 terms after a power of two per row that puts its largest element in
 // [128, 256): hi is q rounded to e4m3, lo the remainder, exact for every element of at least 2^-10 of
 // the row's largest. Four more warps widen the V codes to bf16 (exact). The K scale and the row's power
-// of two multiply S, the V scale the weight before its rounding: they and the widening cost 423 us
-// where bf16 takes 237 (without the scales 355). 32 x 1 queries behind 131,072 rows: 116 us, 106 without the K
+// of two multiply S, the V scale the weight before its rounding: they and the widening cost 411 us
+// where bf16 takes 217. 32 x 1 queries behind 131,072 rows: 116 us, 106 without the K
 // scales, 109 without the V scales, 101 without the widening, 82 without all three; bf16 66. No pipe is
 // busy for half the time (tensor 39 %, shared memory's loads and stores 41 %, special functions 28 %): a
 // warp's chain through a half tile is longer, 2,300 to 3,500 clocks. A quarter of the columns of four rows per
