@@ -103,6 +103,23 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Eight elements of a row that starts anywhere, by pairs, behind the first element where that is an odd one.
+// (13,674 x 973 x 128 in bf16: 18.5 us, with a row's elements by neighbouring lanes, one at a time, 30.)
+__device__ __forceinline__ void store_piece(__nv_bfloat16 *o, uint4 u) {
+  const bool odd = reinterpret_cast<uintptr_t>(o) & 2;
+  uint32_t *p = reinterpret_cast<uint32_t *>(o + odd);
+  p[0] = odd ? __byte_perm(u.x, u.y, 0x5432) : u.x;
+  p[1] = odd ? __byte_perm(u.y, u.z, 0x5432) : u.y;
+  p[2] = odd ? __byte_perm(u.z, u.w, 0x5432) : u.z;
+  if (odd) {
+    uint16_t *h = reinterpret_cast<uint16_t *>(o);
+    h[0] = (uint16_t)u.x;
+    h[7] = (uint16_t)(u.w >> 16);
+  } else {
+    p[3] = u.w;
+  }
+}
+
 // One warp's 32 rows x 128 bytes through its square of shared memory: lane = row writes its 8
 // pieces of 16 bytes (swizzled), then each row leaves by 8 neighbouring lanes. `cols`: elements of
 // the row that exist.
@@ -131,10 +148,23 @@ __device__ __forceinline__ void store_square(uint8_t *sq, const uint4 (&v)[8], T
             if (c * per + i < cols) o[i] = e[i];
         }
       }
-  } else {
+  } else if constexpr (sizeof(T) == 4) {   // a row per instruction
     for (int r = 0; r < min(rows, 32); ++r)
-      for (int c = lane; c < min(cols, 8 * per); c += 32)
-        out[r * ldo + c] = *reinterpret_cast<const T *>(sq + sw128(r, c * (int)sizeof(T)));
+      if (lane < cols) out[r * ldo + lane] = *reinterpret_cast<const T *>(sq + sw128(r, lane * 4));
+  } else {
+    const int c = lane & 7, left = cols - c * per;
+    T *o = out + (lane >> 3) * ldo + c * per;
+#pragma unroll 1
+    for (int r = lane >> 3; r < min(rows, 32); r += 4, o += 4 * ldo) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(sq + sw128(r, c * 16));
+      if (left >= per) {
+        store_piece(o, u);
+      } else {
+        const T *e = reinterpret_cast<const T *>(sq + sw128(r, c * 16));
+#pragma unroll 1
+        for (int i = 0; i < left; ++i) o[i] = e[i];
+      }
+    }
   }
 }
 
