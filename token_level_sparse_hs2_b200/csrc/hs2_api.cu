@@ -1633,8 +1633,9 @@ struct PrefixPlan {
 
 // Every pair of row blocks walks its tiles (the prefix's and its sequences' own) in n_splits
 // ranges. Fewer ranges mean fewer partial results, more fill the last wave of CTAs better: the
-// count with the least time, a CTA costing its tiles and about six tiles' time more (set-up, first
-// loads, the result).
+// count with the least time, a CTA costing its tiles and about six bf16 tiles' time more (set-up, first
+// loads, the result), and each range a sixteenth of one in the merge (16 rows behind 55,624: 146 ranges of 3
+// tiles 20.7 us, 88 of 5 17.0). A tile of e4m3 takes more (96 rows behind 8,328: 66 ranges 14.4 us, 33 15.4).
 PrefixPlan prefix_plan(const hs2_kv_view *kv, int32_t prefix_len) {
   PrefixPlan F;
   const int64_t per_seq = (int64_t)kv->n_q * kv->n_heads;
@@ -1651,7 +1652,7 @@ PrefixPlan prefix_plan(const hs2_kv_view *kv, int32_t prefix_len) {
   int64_t best = INT64_MAX;
   for (int s = 1; s <= (int)std::min<int64_t>(kPxMaxSplits, tiles); ++s) {
     const int64_t waves = ((int64_t)F.n_pairs * s + kPrefixCtas - 1) / kPrefixCtas;
-    const int64_t cost = waves * ((tiles + s - 1) / s + 6);
+    const int64_t cost = waves * ((tiles + s - 1) / s * (kv->kv_dtype == HS2_KV_BF16 ? 16 : 40) + 96) + s;
     if (cost < best) {
       best = cost;
       F.n_splits = s;
