@@ -208,15 +208,16 @@ __device__ __forceinline__ void px_split_q(uint4 v, uint8_t *qb, int r, int ch, 
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   // exponents kept in the range whose powers of two are normal both ways
-  const int ex = amax > 0.f ? min(max(ilogbf(amax) - 7, -120), 120) : 0;
+  const int ex = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 134, -120), 120) : 0;
   const float down = __int_as_float((127 - ex) << 23);
+  const float2 down2 = make_float2(down, down);
   uint32_t hi[2], lo[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t h[2], l[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float2 x = make_float2(f[4 * i + 2 * j] * down, f[4 * i + 2 * j + 1] * down);
+      const float2 x = fmul2(make_float2(f[4 * i + 2 * j], f[4 * i + 2 * j + 1]), down2);
       const __nv_fp8x2_storage_t hc = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
       const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hc, __NV_E4M3);
       const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
@@ -243,6 +244,21 @@ __device__ __forceinline__ void px_scale(float (&x)[32], const float *ksc) {
     x[i + 1] = a.y;
     x[i + 2] = b.x;
     x[i + 3] = b.y;
+  }
+}
+
+// A warp's rows (a multiple of 16, as the heads are) from shared memory, four columns per lane, eight rows read
+// before the first is stored (one at a time 2 x 1 queries behind 1,000 rows took 8.6 us, so 8.1).
+template <class Store>
+__device__ __forceinline__ void store_rows(const uint8_t *mem, int rows, Store store) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    float4 f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const float4 *>(mem + (r0 + i) * kPxOutRow + lane * 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) store(r0 + i, f[i]);
   }
 }
 
@@ -339,7 +355,7 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int r = r0 + 16 * i;
-        px_split_q(v[i], sm.q + (r >> 7) * (kPxRows * 256), r & 127, ch, P.scale_log2, sm.qscale + r);
+        if (i < 8 || nb == 2) px_split_q(v[i], sm.q + (r >> 7) * (kPxRows * 256), r & 127, ch, P.scale_log2, sm.qscale + r);
       }
       fence_proxy_async_smem();
     }
@@ -726,16 +742,12 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
     const int rows_w = (int)min((int64_t)32, P.rows - first);
     if (!whole || P.out_f32) {
       float *o = (whole ? static_cast<float *>(P.out) : P.part_o + (int64_t)split * P.rows * kHeadDim) + first * kHeadDim;
-#pragma unroll 8
-      for (int r = 0; r < rows_w; ++r)
-        *reinterpret_cast<float4 *>(o + r * kHeadDim + lane * 4) = *reinterpret_cast<const float4 *>(mem + r * kPxOutRow + lane * 16);
+      store_rows(mem, rows_w, [&](int r, const float4 &f) { *reinterpret_cast<float4 *>(o + r * kHeadDim + lane * 4) = f; });
     } else {
       __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(P.out) + first * kHeadDim;
-#pragma unroll 8
-      for (int r = 0; r < rows_w; ++r) {
-        const float4 f = *reinterpret_cast<const float4 *>(mem + r * kPxOutRow + lane * 16);
+      store_rows(mem, rows_w, [&](int r, const float4 &f) {
         *reinterpret_cast<uint2 *>(o + r * kHeadDim + lane * 4) = make_uint2(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w));
-      }
+      });
     }
     const float lse = some ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     if (row < P.rows) {
