@@ -19,7 +19,7 @@
 // O is rescaled in TMEM. P is rounded to bf16 (the tensor cores take no wider operand next to bf16 V;
 // half a step, 2^-8 of each weight, averaged over the keys); m, the sums and O are float32.
 //
-// What bounds it: 4 x 128 queries x 32 heads behind 30,001 rows take 217 us (1,160 TFLOP/s, 0.69 of the
+// What bounds it: 4 x 128 queries x 32 heads behind 30,001 rows take 213 us (1,185 TFLOP/s, 0.71 of the
 // measured bf16 rate); the tensor pipe is active 64 % of the time, its operand reads take 61 % of
 // shared memory's cycles (S with 64 columns reads Q for every 64 keys), the special-function unit is
 // busy 64 %: each waits for the others at times, and none alone is the limit. Slower were S in one piece of 128
@@ -31,8 +31,8 @@
 // query split into two e4m3 terms after a power of two per row that puts its largest element in
 // [128, 256): hi is q rounded to e4m3, lo the remainder, exact for every element of at least 2^-10 of
 // the row's largest. Four more warps widen the V codes to bf16 (exact). The K scale and the row's power
-// of two multiply S, the V scale the weight before its rounding: they and the widening cost 411 us
-// where bf16 takes 217. 32 x 1 queries behind 131,072 rows: 116 us, 106 without the K
+// of two multiply S, the V scale the weight before its rounding: they and the widening cost 403 us
+// where bf16 takes 213. 32 x 1 queries behind 131,072 rows: 116 us, 106 without the K
 // scales, 109 without the V scales, 101 without the widening, 82 without all three; bf16 66. No pipe is
 // busy for half the time (tensor 39 %, shared memory's loads and stores 41 %, special functions 28 %): a
 // warp's chain through a half tile is longer, 2,300 to 3,500 clocks. A quarter of the columns of four rows per
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
 // out = sum_j w_j O_j / sum_j w_j, w_j = exp(lse_j - max lse), over the ranges of a row's tiles. kW warps
 // share a row: each sums every kW-th part, four columns per lane, and the warps' sums meet in shared
 // memory, in warp order. Few rows take eight warps each, many one for each four parts or so: with eight, 16,384
-// rows of two parts took 29 us of instructions (4 x 128 queries behind 30,001 rows 234 us in all, now 217).
+// rows of two parts took 29 us of instructions (4 x 128 queries behind 30,001 rows 234 us in all, 217 so).
 constexpr int kPmWarps = 8;           // per CTA
 
 template <int kW>
