@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -47,10 +48,15 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return res.stderr
 
 
+def _marshal_stamp() -> str:
+    """What marshal.cpp.o depends on besides its sources: the torch and the Python it is compiled against."""
+    import torch
+    return "\n".join([torch.__version__, os.path.dirname(torch.__file__), str(torch._C._GLIBCXX_USE_CXX11_ABI),
+                      str(sysconfig.get_config_var("EXT_SUFFIX")), sysconfig.get_paths()["include"]])
+
+
 def _marshal_object(src: str, obj: str) -> None:
     """Compiles marshal.cpp against torch's headers."""
-    import sysconfig
-
     import torch
     inc = [os.path.join(os.path.dirname(torch.__file__), "include"), sysconfig.get_paths()["include"],
            os.path.join(ROOT, "include")]
@@ -73,6 +79,27 @@ def _marshal_link(obj: str) -> None:
     os.replace(tmp, MARSHAL)
 
 
+def _link(objs) -> None:
+    tmp = LIB + f".tmp{os.getpid()}"
+    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{res.stderr}")
+    os.replace(tmp, LIB)
+
+
+def _older(path: str, than) -> bool:
+    """Whether `path` is missing or older than one of the files."""
+    return not os.path.exists(path) or os.path.getmtime(path) < max(os.path.getmtime(p) for p in than)
+
+
+def _read(path: str):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -85,27 +112,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or not os.path.exists(obj) or \
                 os.path.getmtime(obj) < max(os.path.getmtime(src), dep_mtime):
             jobs.append((src, obj))
+    # The module is made anew when its sources, torch or Python have changed, and linked anew whenever it is older
+    # than its object (an earlier call may have failed in between): after a change of hs2.h an older one would
+    # call the library with the arguments of before.
     msrc, mobj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.cpp.o")
-    m_deps = max(os.path.getmtime(msrc), os.path.getmtime(os.path.join(ROOT, "include", "hs2.h")))
-    m_job = force or not os.path.exists(mobj) or os.path.getmtime(mobj) < m_deps
-    if jobs or m_job:
-        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
-            marshal = ex.submit(_marshal_object, msrc, mobj) if m_job else None
-            logs = list(ex.map(lambda j: _compile(j[0], j[1], verbose), jobs))
-            if marshal is not None:
-                marshal.result()
-        if verbose:
-            for log in logs:
-                sys.stderr.write(log)
-    if force or jobs or not os.path.exists(LIB):
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"link failed:\n{res.stderr}")
-        os.replace(tmp, LIB)
-    if m_job or not os.path.exists(MARSHAL):
-        _marshal_link(mobj)
+    mstamp, stamp = os.path.join(BUILD, "marshal.stamp"), _marshal_stamp()
+    m_job = force or _older(mobj, [msrc, os.path.join(ROOT, "include", "hs2.h")]) or _read(mstamp) != stamp
+    try:
+        if jobs or m_job:
+            with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
+                marshal = ex.submit(_marshal_object, msrc, mobj) if m_job else None
+                logs = list(ex.map(lambda j: _compile(j[0], j[1], verbose), jobs))
+                if marshal is not None:
+                    marshal.result()
+                    with open(mstamp, "w") as f:
+                        f.write(stamp)
+            if verbose:
+                for log in logs:
+                    sys.stderr.write(log)
+        if force or _older(LIB, objs):
+            _link(objs)
+        if force or _older(MARSHAL, [mobj]):
+            _marshal_link(mobj)
+    except BaseException:
+        # no module that does not match what is (or the next call finds) built
+        if os.path.exists(MARSHAL) and (m_job or _older(MARSHAL, [mobj])):
+            os.remove(MARSHAL)
+        raise
     return LIB
 
 
