@@ -16,7 +16,7 @@ def tree(tmp_path, monkeypatch):
     (here / "csrc").mkdir(parents=True)
     inc.mkdir()
     t = types.SimpleNamespace(kernel=here / "csrc" / "k.cu", module=here / "csrc" / "marshal.cpp", header=inc / "hs2.h",
-                              lib=here / "libhs2.so", marshal=here / "_marshal.so", runs=[], broken=(), clock=1_000_000_000)
+                              lib=here / "libhs2.so", marshal=here / "_marshal.so", runs=[], broken=(), missing=(), clock=1_000_000_000)
     for f in (t.kernel, t.module, t.header):
         f.write_text("")
     for name, value in (("HERE", here), ("ROOT", tmp_path), ("CSRC", here / "csrc"), ("BUILD", here / "_build"), ("LIB", t.lib),
@@ -31,6 +31,8 @@ def tree(tmp_path, monkeypatch):
         out = cmd[cmd.index("-o") + 1]
         name = os.path.basename(out).split(".tmp")[0]
         t.runs.append(name)
+        if os.path.basename(cmd[0]) in t.missing:
+            raise FileNotFoundError(cmd[0])
         if name in t.broken:
             return subprocess.CompletedProcess(cmd, 1, "", "broken")
         with open(out, "w") as f:
@@ -46,7 +48,7 @@ def tree(tmp_path, monkeypatch):
         t.runs.clear()
         t.broken = broken
         if fails:
-            with pytest.raises(RuntimeError):
+            with pytest.raises((RuntimeError, OSError)):
                 B.build()
         else:
             B.build()
@@ -83,6 +85,24 @@ def test_no_older_module_beside_a_new_library(tree, broken):
     tree.change(tree.header, "new signature")
     tree.build(broken=(broken,), fails=True)
     assert tree.lib.exists() and (tree.lib.read_text() == "" or not tree.marshal.exists())
+
+
+def test_the_library_needs_no_torch(tree, monkeypatch):
+    import sys
+    tree.change(tree.header, "new signature")
+    monkeypatch.setitem(sys.modules, "torch", None)                  # import torch raises ImportError
+    assert tree.build() == {"k.cu.o", "libhs2.so"}
+    assert tree.lib.read_text() == "new signature" and not tree.marshal.exists()
+    monkeypatch.undo()
+
+
+def test_the_library_needs_no_host_compiler_of_the_module(tree):
+    tree.change(tree.header, "new signature")
+    tree.missing = ("g++",)
+    tree.build(fails=True)                                           # says so, with the library built
+    assert tree.lib.read_text() == "new signature" and not tree.marshal.exists()
+    tree.missing = ()
+    assert tree.build() == {"marshal.cpp.o", "_marshal.so"}
 
 
 def test_another_torch_is_a_new_module(tree, monkeypatch):

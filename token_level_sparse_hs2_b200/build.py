@@ -1,5 +1,6 @@
 """Builds libhs2.so (the CUDA kernels + C ABI) in-tree for sm_100a with nvcc, and the Python module
-_marshal.so (csrc/marshal.cpp: torch tensors to C ABI calls) against it with the host compiler.
+_marshal.so (csrc/marshal.cpp: torch tensors to C ABI calls) against it with the host compiler. The
+library needs nvcc alone: it is linked whether or not the module can be made, and without torch the module is left out.
 
 Usage: python -m token_level_sparse_hs2_b200.build [--force]
 Object files go to token_level_sparse_hs2_b200/_build/; the library to
@@ -48,9 +49,13 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return res.stderr
 
 
-def _marshal_stamp() -> str:
-    """What marshal.cpp.o depends on besides its sources: the torch and the Python it is compiled against."""
-    import torch
+def _marshal_stamp():
+    """What marshal.cpp.o depends on besides its sources: the torch and the Python it is compiled against. None
+    without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     return "\n".join([torch.__version__, os.path.dirname(torch.__file__), str(torch._C._GLIBCXX_USE_CXX11_ABI),
                       str(sysconfig.get_config_var("EXT_SUFFIX")), sysconfig.get_paths()["include"]])
 
@@ -116,27 +121,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
     # than its object (an earlier call may have failed in between): after a change of hs2.h an older one would
     # call the library with the arguments of before.
     msrc, mobj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.cpp.o")
+    mdeps = [msrc, os.path.join(ROOT, "include", "hs2.h")]
     mstamp, stamp = os.path.join(BUILD, "marshal.stamp"), _marshal_stamp()
-    m_job = force or _older(mobj, [msrc, os.path.join(ROOT, "include", "hs2.h")]) or _read(mstamp) != stamp
+    m_job = stamp is not None and (force or _older(mobj, mdeps) or _read(mstamp) != stamp)
     try:
-        if jobs or m_job:
-            with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
-                marshal = ex.submit(_marshal_object, msrc, mobj) if m_job else None
-                logs = list(ex.map(lambda j: _compile(j[0], j[1], verbose), jobs))
-                if marshal is not None:
-                    marshal.result()
-                    with open(mstamp, "w") as f:
-                        f.write(stamp)
-            if verbose:
-                for log in logs:
-                    sys.stderr.write(log)
+        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
+            marshal = ex.submit(_marshal_object, msrc, mobj) if m_job else None
+            logs = list(ex.map(lambda j: _compile(j[0], j[1], verbose), jobs))
+        if verbose:
+            for log in logs:
+                sys.stderr.write(log)
         if force or _older(LIB, objs):
             _link(objs)
-        if force or _older(MARSHAL, [mobj]):
+        if marshal is not None:
+            marshal.result()
+            with open(mstamp, "w") as f:
+                f.write(stamp)
+        if stamp is None:
+            sys.stderr.write("torch cannot be imported: libhs2.so is built, the Python module _marshal.so is not\n")
+            if os.path.exists(MARSHAL) and _older(MARSHAL, mdeps):
+                os.remove(MARSHAL)
+        elif force or _older(MARSHAL, [mobj]):
             _marshal_link(mobj)
     except BaseException:
         # no module that does not match what is (or the next call finds) built
-        if os.path.exists(MARSHAL) and (m_job or _older(MARSHAL, [mobj])):
+        if os.path.exists(MARSHAL) and (m_job or _older(MARSHAL, mdeps)):
             os.remove(MARSHAL)
         raise
     return LIB
