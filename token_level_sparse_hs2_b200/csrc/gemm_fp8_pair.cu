@@ -229,6 +229,9 @@ __global__ void __launch_bounds__(kGpThreads, 1)
         __syncwarp();
       }
     }
+    // The leader's products hand the last stages back in both CTAs: each sees these arrivals before it ends.
+    for (int j = max(0, it - kGpStages); j < it && ok; ++j)
+      ok = warp_wait_all(P.status, sm.abort_flag, &sm.empty[j % kGpStages], (j / kGpStages) & 1);
     if (!ok) {   // gave up: copies in flight land before the CTA ends (they take microseconds)
       const uint64_t t0 = globaltimer();
       while (globaltimer() - t0 < 1000000ull) {}
@@ -371,6 +374,10 @@ __global__ void __launch_bounds__(kGpThreads, 1)
     }
   }
   tc_fence_before();
+  __syncthreads();
+  // The leader's last commit arrives here too, and a cluster barrier does not order it: the memory of a CTA that
+  // has ended may be the next kernel's already.
+  if (rank == 1 && threadIdx.x == 0 && !mbar_wait(smem_u32(&sm.done[0]), 0)) record_status(P.status, kStatusTimeout);
   __syncthreads();
   cluster_sync_all();   // the pair's products and copies are over in both CTAs
   if (warp == kGpWarpMma) {
