@@ -317,9 +317,11 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
     fence_barrier_init();
   }
   if (warp == kPxWarpTma && lane == 0) {
-    prefetch_tensormap(&tm.q);
-    prefetch_tensormap(&tm.pk);
-    prefetch_tensormap(&tm.pv);
+    if constexpr (!C::kFp8) prefetch_tensormap(&tm.q);   // (the maps that the host has made)
+    if (P.n_tiles > 0) {
+      prefetch_tensormap(&tm.pk);
+      prefetch_tensormap(&tm.pv);
+    }
     prefetch_tensormap(&tm.k);
     prefetch_tensormap(&tm.v);
   }

@@ -220,8 +220,8 @@ struct PrefixParams {
   uint32_t *status;           // cleared by the first CTA
 };
 struct PrefixMaps {
-  CUtensorMap q;              // [rows, 128], boxes of 128 rows x 64 (bf16 caches)
-  CUtensorMap pk, pv;         // the prefix's rows alone; boxes of 128 rows x 128 bytes
+  CUtensorMap q;              // [rows, 128], boxes of 128 rows x 64 (e4m3 caches: not made)
+  CUtensorMap pk, pv;         // the prefix's rows alone (none: not made); boxes of 128 rows x 128 bytes
   CUtensorMap k, v;           // the whole cache
 };
 cudaError_t launch_prefix_attn(int kv_dtype, const PrefixMaps &tm, const PrefixParams &p, cudaStream_t s);
