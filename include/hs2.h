@@ -389,7 +389,8 @@ hs2_status hs2_fp8_quantize(int64_t rows, int32_t cols, const void *x, int64_t x
  * a: device codes [m, k] with 1 x 128 scales (activations: hs2_rms_norm, hs2_fp8_quantize with
  * block_rows 1), w: device codes [n, k], output feature x input feature, with 128 x 128 scales
  * (hs2_fp8_quantize with block_rows 128). Codes 16-byte aligned, lda and ldw >= k multiples of 16;
- * scales [kb, *_scale_ld], 16-byte aligned. k: a multiple of 16 in [16, 65536]; n in [1, 2^24];
+ * a_scale [kb, a_scale_ld], 16-byte aligned, a_scale_ld as above; w_scale [kb, w_scale_ld] with any
+ * start and any w_scale_ld >= ceil(n / 128) (a slice of a larger matrix's scales). k: a multiple of 16 in [16, 65536]; n in [1, 2^24];
  * m 0: nothing is launched. out: device [m, n] of out_dtype with row stride ldo >= n, aligned to
  * its element; with ldo * element size a multiple of 16 and out 16-byte aligned it is stored in
  * wide pieces. Elements between n and ldo and rows from m on are not written. workspace: device,

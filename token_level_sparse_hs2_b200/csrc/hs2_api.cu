@@ -1389,15 +1389,22 @@ hs2_status hs2_kv_bridge(const hs2_kv_view *kv, const void *hidden, int32_t d_mo
 namespace {
 bool out_type(int t) { return t == HS2_OUT_BF16 || t == HS2_OUT_F32; }
 
-hs2_status check_codes(int64_t row_blocks, int cols, const void *codes, int64_t stride,
-                       const float *scales, int64_t scale_ld) {
-  if (!codes || !scales) return fail(HS2_ERR_INVALID_ARG, "codes / scales is NULL");
-  if (!aligned16(codes) || !aligned16(scales))
-    return fail(HS2_ERR_INVALID_ARG, "codes / scales must be 16-byte aligned");
+hs2_status check_code_rows(int cols, const void *codes, int64_t stride) {
+  if (!codes) return fail(HS2_ERR_INVALID_ARG, "codes / scales is NULL");
+  if (!aligned16(codes)) return fail(HS2_ERR_INVALID_ARG, "codes / scales must be 16-byte aligned");
   if (cols % 16) return fail(HS2_ERR_UNSUPPORTED, "%d columns of codes (a multiple of 16)", cols);
   if (stride < cols || stride % 16)
     return fail(HS2_ERR_INVALID_ARG, "codes_stride %lld (a multiple of 16, at least %d)",
                 (long long)stride, cols);
+  return HS2_OK;
+}
+
+hs2_status check_codes(int64_t row_blocks, int cols, const void *codes, int64_t stride,
+                       const float *scales, int64_t scale_ld) {
+  if (!scales) return fail(HS2_ERR_INVALID_ARG, "codes / scales is NULL");
+  if (!aligned16(scales)) return fail(HS2_ERR_INVALID_ARG, "codes / scales must be 16-byte aligned");
+  const hs2_status st = check_code_rows(cols, codes, stride);
+  if (st != HS2_OK) return st;
   if (scale_ld < row_blocks || scale_ld % 4)
     return fail(HS2_ERR_INVALID_ARG, "scale_ld %lld (a multiple of 4, at least %lld)",
                 (long long)scale_ld, (long long)row_blocks);
@@ -1569,7 +1576,11 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
   if (m == 0) return ok();
   if (!w || !w_scale || !out) return fail(HS2_ERR_INVALID_ARG, "w / w_scale / out is NULL");
   if ((st = check_codes(m, k, a, lda, a_scale, a_scale_ld)) != HS2_OK) return st;
-  if ((st = check_codes((n + 127) / 128, k, w, ldw, w_scale, w_scale_ld)) != HS2_OK) return st;
+  if ((st = check_code_rows(k, w, ldw)) != HS2_OK) return st;
+  // the kernels read the weights' scales one by one
+  if (reinterpret_cast<uintptr_t>(w_scale) % 4) return fail(HS2_ERR_INVALID_ARG, "w_scale is not aligned to its element");
+  if (w_scale_ld < (n + 127) / 128)
+    return fail(HS2_ERR_INVALID_ARG, "w_scale: scale_ld %lld (at least %d)", (long long)w_scale_ld, (n + 127) / 128);
   if (ldo < n) return fail(HS2_ERR_INVALID_ARG, "ldo %lld < n = %d", (long long)ldo, n);
   const int oe = out_dtype == HS2_OUT_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(out) % oe) return fail(HS2_ERR_INVALID_ARG, "out is not aligned to its element");
