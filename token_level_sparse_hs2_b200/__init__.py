@@ -173,6 +173,22 @@ class KvCache:
             raise TypeError(f"unsupported cache dtype {k.dtype}")
         if not (k.is_contiguous() and v.is_contiguous()) or k.shape != v.shape or k.dim() != 2:
             raise ValueError("k and v must be contiguous [rows, 128] tensors of one shape")
+        # the calls pass addresses on: what they would read past its end or as another type stops here
+        if (v.dtype == torch.bfloat16) != (k.dtype == torch.bfloat16) or \
+                v.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+            raise TypeError(f"v is {v.dtype}, k {k.dtype}")
+        if v.device != k.device:
+            raise ValueError(f"v is on {v.device}, k on {k.device}")
+        if self.kv_dtype == KV_FP8_E4M3:
+            for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if s is None:
+                    continue                      # (refused by the calls)
+                if s.dtype != torch.float32:
+                    raise TypeError(f"{name} is {s.dtype}, not float32")
+                if not s.is_contiguous() or s.numel() < k.shape[0]:
+                    raise ValueError(f"{name} must be contiguous, one element per row of k")
+                if s.device != k.device:
+                    raise ValueError(f"{name} is on {s.device}, k on {k.device}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.kv_start = (ctypes.c_int64 * len(kv_start))(*[int(x) for x in kv_start])
         self.kv_len = (ctypes.c_int32 * len(kv_len))(*[int(x) for x in kv_len])
