@@ -723,9 +723,11 @@ __global__ void __launch_bounds__(PxCfg<KV>::kThreads, 1)
   const bool aborted = *sm.abort_flag != 0;
   if (warp < 8 && g < nb && !aborted) {
     // ------------------------------------------------------------ O and log-sum-exp
-    const bool some = m_run != -INFINITY || l_run != 0.f;   // a row may see nothing in this range
-    const float inv = some ? 1.f / l_run : 0.f;
     const bool whole = P.n_splits == 1;
+    // A row may see nothing in this range. (With one range it sees its own position at least: a sum of zero is that
+    // of scores of -inf, and the result the NaN of the formula, as the merge's.)
+    const bool some = whole || m_run != -INFINITY || l_run != 0.f;
+    const float inv = some ? 1.f / l_run : 0.f;
     // through shared memory (the tiles are done with), a warp's 32 rows at a time, so that rows leave
     // in one piece: a thread storing its own row took 6 us
     uint8_t *mem = sm.q + warp * kPxOutWarp;
