@@ -1,6 +1,6 @@
 """hs2_prefix_attn within bounds that count each rounding of the kernel once.
 
-The scores here are sums of products of small whole numbers (times powers of two), so the
+The scores of most cases here are sums of products of small whole numbers (times powers of two), so the
 tensor cores' sums are exact and what is left is arithmetic that can be bounded. With z = score / ln 2 and the
 largest |z| of a row Z, T keys and n = T / 128 + 2 tiles:
 
@@ -13,7 +13,12 @@ largest |z| of a row Z, T keys and n = T / 128 + 2 tiles:
   output    each weight (times its V scale, one product) rounded to bf16 once, 2^-8; dw for the weight and dw for
             the sum; T additions of the tensor cores within 2^-23 of the magnitude so far (truncation
             allowed); the sum's additions as above; the ranges' weights, within the lse's error, twice; all
-            of a = sum of weight x |v|; then the output's half step (bf16 2^-8, float32 2^-24)."""
+            of a = sum of weight x |v|; then the output's half step (bf16 2^-8, float32 2^-24).
+
+The e4m3 cache's query is held as two e4m3 terms after a power of two that puts the row's largest element in
+[128, 256). An element of at least 2^-9 of the largest is at least 1/4 then: its bf16 steps, 2^-9 or more, are
+within reach of the second term, and the sum is exact. Of a smaller one the last bits below 2^-9 are lost:
+at most 2^-10 of the scaled unit, 2^-17 of the row's largest element."""
 import math
 
 import pytest
@@ -56,7 +61,8 @@ def whole_numbers(c, fp8, seed):
         c.k = kb.cuda()
 
 
-def check(c, got, lse):
+def check(c, got, lse, score_error=None):
+    """score_error(q, k): a bound of what the scores' sums lose, [H, T] of q [H, 128] and k [T, 128]."""
     for b, (f, t) in enumerate(zip(c.first, c.lens)):
         for i in range(c.n_q):
             rows = torch.cat([torch.arange(c.start, c.start + c.prefix), torch.arange(f, f + t - c.n_q + i + 1)])
@@ -65,6 +71,8 @@ def check(c, got, lse):
             T, z = len(rows), (x.abs().amax(1) / math.log(2))
             tiles = T / 128 + 2
             dw = math.log(2) * (5 * z + 8) * 2.0 ** -24 + 2.0 ** -22
+            if score_error is not None:
+                dw = dw + score_error(q, k).amax(1)
             want = torch.logsumexp(x, 1)
             tol = dw + (94 + 2 * tiles) * 2.0 ** -24 + 2 * tiles * (2.0 ** -22 + 2.0 ** -24) + 2.0 ** -20 + 2.0 ** -21 * want.abs()
             off = (lse[b, i].cpu().double() - want).abs()
@@ -109,3 +117,26 @@ def test_growing_and_falling_scores(fp8, q0):
         c.k[at, 0] = grow.cuda()
     # (other dimensions meet zeros of q)
     check(c, *c.run())
+
+
+def lost_bits(q, k):
+    """What the two e4m3 terms of q lose of each score, and the sums' additions: 2 x 128 products."""
+    top = q.abs().amax(1, keepdim=True)
+    lost = torch.where(q.abs() < 2.0 ** -9 * top, 2.0 ** -17 * top.expand_as(q), torch.zeros_like(q))
+    return C * (lost @ k.abs().t() + 256 * 2.0 ** -23 * (q.abs() @ k.abs().t()))
+
+
+@pytest.mark.parametrize("lens,n_q,prefix", [([40, 50], 1, 700), ([9] * 17, 1, 1300), ([30, 20], 9, 260)])
+@pytest.mark.parametrize("octaves", [8, 10, 12, 20])
+def test_channels_far_above_the_others(lens, n_q, prefix, octaves):
+    """A few channels of every query row 2^8 to 2^20 times the others, in an e4m3 cache."""
+    c = Case(lens, n_q, 32, prefix, True, seed=octaves)
+    g = torch.Generator().manual_seed(octaves)
+    big = torch.rand(c.q.shape, generator=g) < 3 / 128
+    big[..., 7] = True
+    q = torch.randn(c.q.shape, generator=g) * torch.where(big, 2.0 ** octaves, 1.0)
+    c.q = (q * (4.0 / q.abs().amax(-1, keepdim=True))).bfloat16()
+    check(c, *c.run(), score_error=lost_bits)
+    # rows without the large channels
+    c.q = (q.masked_fill(big, 0) * 2.0).bfloat16()
+    check(c, *c.run(), score_error=lost_bits)
