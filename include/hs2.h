@@ -346,7 +346,9 @@ hs2_status hs2_kv_bridge(const hs2_kv_view *kv, const void *hidden, int32_t d_mo
  * i (1 x 128) or rows [128 i, 128 i + 128) (128 x 128); the last block of columns or rows may be
  * shorter. value = scale * code, scale = max|x| / 448 over the block in float32 (1 where that is
  * zero), code = round-to-nearest-even e4m3 of the float32 quotient x / scale: the rule of the
- * e4m3 cache rows. scale_ld is a multiple of 4 and at least the number of rows (of blocks of 128
+ * e4m3 cache rows. A NaN has the code NaN and leaves the scale to the block's other elements; an
+ * infinity makes the scale infinite, its own code NaN and the others 0, so that every value of the
+ * block, and a product with it, is NaN. scale_ld is a multiple of 4 and at least the number of rows (of blocks of 128
  * rows); scales between that number and scale_ld are never written. Strides count elements
  * between rows. Serving only: there are no backward forms. */
 
