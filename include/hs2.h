@@ -413,9 +413,12 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
  * rows may lie anywhere in the cache; kv_rows bounds them too. prefix_len 0: the own rows alone.
  * Cache rows outside the prefix and the sequences are not used, whatever they hold, and one
  * sequence's rows never touch another's results; with n_q > 1 a non-finite V row of a sequence's
- * new tokens may reach the queries before it in the same call. The parts are joined from
- * float32. hs2_score_pass takes the lse for the scores of either part (a view of the own rows,
- * and one whose every sequence is the prefix).
+ * new tokens may reach the queries before it in the same call. For their product with V the weights
+ * (times the V scale, in an e4m3 cache) are rounded to bf16, 2^-8 of each, for either out_dtype; sums,
+ * lse and the joining of the parts are float32. In decode (n_q = 1, which hs2_score_pass is for) the
+ * lse gives the scores of both parts: hs2_score_pass with a view of the own rows, and with one whose
+ * every sequence is the prefix (its shared keys are read once per sequence there). A chunk's call
+ * (n_q > 1) ends here: no pass scores a chunk behind a shared prefix.
  * q: device bf16 [B, n_q, H, 128]; out: device [B, n_q, H, 128] of out_dtype; both 16-byte
  * aligned. lse: device fp32 [B, n_q, H] or NULL. workspace: device, 256-byte aligned, at least
  * hs2_prefix_attn_workspace_size bytes; its contents on entry do not matter. Asynchronous on
