@@ -16,16 +16,21 @@
 // sequence alone: blocks without such rows skip it, and the product leaves the other lanes of O
 // untouched (its output-lane mask), so a row never meets another sequence's values. The reference
 // maximum only moves when a tile's row maximum exceeds it by more than 8 (P <= 2^8); then the row of
-// O is rescaled in TMEM. P is rounded to bf16 (the tensor cores take no wider operand next to bf16 V;
-// half a step, 2^-8 of each weight, averaged over the keys); m, the sums and O are float32.
+// O is rescaled in TMEM. P is rounded to bf16, whatever the output's type (the tensor cores take no wider
+// operand next to bf16 V; half a step, 2^-8 of each weight, averaged over the keys: a relative error of 1.6e-3 of
+// the output, next to the 1.7e-3 of rounding that to bf16); m, the sums and O are float32. For an e4m3 cache f16
+// could hold V's codes exactly too and the weights with three bits more; bf16 is taken for its range, since what
+// is rounded there is the weight times the V scale, and a scale may be as small or large as float32 allows: f16
+// would need a reference scale that moves as the maximum does.
 //
-// What bounds it: 4 x 128 queries x 32 heads behind 30,001 rows take 213 us (1,185 TFLOP/s, 0.71 of the
-// measured bf16 rate); the tensor pipe is active 64 % of the time, its operand reads take 61 % of
+// What bounds it: 4 x 128 queries x 32 heads behind 30,001 rows take 213 us in ten calls or so (1,185 TFLOP/s, 0.71
+// of the measured bf16 rate), 225 in 200 calls and 246 (1,025 TFLOP/s) under the power cap of a long run; the tensor pipe is active 64 % of the time, its operand reads take 61 % of
 // shared memory's cycles (S with 64 columns reads Q for every 64 keys), the special-function unit is
 // busy 64 %: each waits for the others at times, and none alone is the limit. Slower were S in one piece of 128
 // columns without a second buffer (267 us), 16 softmax warps with half the columns each (275 us), one
 // MMA warp for both blocks, and part of the exponentials on the FMA pipe. Few rows behind a long prefix
-// (32 x 1 behind 131,072: 68 us, 0.60 of the rate) add 7 us of set-up and results and the merge's 5.
+// (32 x 1 behind 131,072: 66 us, 0.63 of the rate; with up to 2,048 own rows a sequence 80, three sets of
+// inputs in turn) add 7 us of set-up and results and the merge's 5.
 //
 // An e4m3 cache (value = scale[t] code): S comes from the cached codes as they are (kind::f8f6f4), the
 // query split into two e4m3 terms after a power of two per row that puts its largest element in

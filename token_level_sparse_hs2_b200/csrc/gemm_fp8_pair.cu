@@ -12,8 +12,8 @@
 //   warp 8      TMEM owner; in the leader (rank 0) also the MMA issuer for both
 //   warps 10, 11  nothing (the register split goes by groups of four warps)
 //   warps 0..7  epilogue: warp w has lanes 32 (w % 4) .. + 31 and features 128 (w / 4) .. + 127
-// What bounds it: 32768 x 4096 x 4096 takes 505 to 525 us (2.1 to 2.2 PFLOP/s, 0.63 to 0.65 of twice the
-// measured bf16 rate; under the power cap of a long run 600 us). The products and loads alone (accumulators
+// What bounds it: 32768 x 4096 x 4096 takes 505 to 525 us in ten calls or so (2.1 to 2.2 PFLOP/s, 0.63 to 0.65 of
+// twice the measured bf16 rate), 548 in 200 calls, about 600 (1.8 PFLOP/s) under the power cap of a long run. The products and loads alone (accumulators
 // handed back unread) take 411 us, reading and adding them (with a quarter of the products) 441 us: two
 // accumulators, all of TMEM, do not hide one behind the other altogether. The epilogue warps are busy
 // throughout: of about 830 clocks a block 190 go to the barrier, 70 to the first columns, 390 to the rest. No

@@ -1633,7 +1633,7 @@ hs2_status hs2_gemm_fp8(int64_t m, int32_t n, int32_t k, const void *a, int64_t 
 
 namespace {
 constexpr int kPrefixTile = 128;          // prefix rows per tile, and (query, head) rows per block
-constexpr int kPrefixCtas = 148;          // one CTA per SM
+constexpr int kPrefixCtas = 148;          // one CTA per SM (a number: the workspace's size is known without a device)
 
 // Work split and workspace of hs2_prefix_attn.
 struct PrefixPlan {
