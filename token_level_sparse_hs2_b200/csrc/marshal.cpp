@@ -104,6 +104,7 @@ void *dense(const char *name, PyObject *o, Types types, at::IntArrayRef shape, i
 void *buffer(const char *name, PyObject *o, int device, size_t *bytes) {
   const at::TensorBase &t = tensor(name, o);
   on_device(name, t, device);
+  if (!t.is_non_overlapping_and_dense()) refuse(PyExc_ValueError, std::string(name) + " must be one piece of memory");
   *bytes = t.nbytes();
   return t.mutable_data_ptr();
 }
