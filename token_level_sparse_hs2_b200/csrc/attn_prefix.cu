@@ -235,7 +235,9 @@ __device__ __forceinline__ void px_split_q(uint4 v, uint8_t *qb, int r, int ch, 
   *reinterpret_cast<uint2 *>(qb + sw128(r, ch * 8)) = make_uint2(hi[0], hi[1]);
   *reinterpret_cast<uint2 *>(qb + kPxRows * 128 + sw128(r, ch * 8)) = make_uint2(lo[0], lo[1]);
   // an infinite element has no such terms: every score of its row is infinite or NaN, and so its softmax NaN
-  if (ch == 0) *factor = amax == INFINITY ? __int_as_float(0x7fc00000) : scale_log2 * __int_as_float((127 + ex) << 23);
+  // (the factor stays above zero, which would make NaN of the -inf of masked columns)
+  if (ch == 0)
+    *factor = amax == INFINITY ? __int_as_float(0x7fc00000) : fmaxf(scale_log2 * __int_as_float((127 + ex) << 23), 0x1p-149f);
 }
 
 // 32 scores of this thread's row times their K scales (e4m3).
