@@ -442,7 +442,8 @@ def fp8_quantize(x, codes, scales, block_rows: int = 1, stream=None):
 
 def gemm_fp8(a, a_scale, w, w_scale, out, workspace, stream=None):
     """out = A W^T of e4m3 codes a [m, k] (1 x 128 scales) and w [n, k] (128 x 128 scales), in
-    float32, rounded to out's type (hs2_gemm_fp8). workspace: at least 256 bytes."""
+    float32, rounded to out's type (hs2_gemm_fp8). w and w_scale may be slices of a fused projection's.
+    workspace: at least 256 bytes."""
     dev = _device()
     st = _calls().gemm_fp8(a, a_scale, w, w_scale, out, workspace, dev, _stream_on(dev, stream))
     if st:
